@@ -64,7 +64,10 @@ EXPORTS = ("bsgemm_fp8_nt", "bsgemm_fp8_tn", "bsgemm_fp8_nn", "bsgemm_fp8_tt", "
            "bsgemm_fp8_gemm_fmt", "bsgemm_fp8_gemm_fused", "bsgemm_fp8_grouped_nt",
            "bsgemm_make_plan", "bsgemm_status_string", "bsgemm_get_last_device_status",
            "bsgemm_last_device_status_detail", "bsgemm_diag_wait_timeout", "bsgemm_version",
-           "bsgemm_fp8_nt_noalloc", "bsgemm_quantize_fp8", "bsgemm_release_workspaces")
+           "bsgemm_fp8_nt_noalloc", "bsgemm_quantize_fp8", "bsgemm_release_workspaces",
+           "bsgemm_fp8_gemm_residual", "bsgemm_rms_norm_quantize_fp8", "bsgemm_rms_norm_backward",
+           "bsgemm_rms_norm_backward_workspace", "bsgemm_activation_quantize_fp8",
+           "bsgemm_activation_backward_quantize_fp8", "bsgemm_activation_backward_workspace")
 
 
 def lib():
@@ -108,6 +111,23 @@ def lib():
             L.bsgemm_quantize_fp8.restype = i32
             L.bsgemm_release_workspaces.argtypes = []
             L.bsgemm_release_workspaces.restype = i32
+            L.bsgemm_fp8_gemm_residual.argtypes = [i32, i32, i32, p, p, p, p, ctypes.POINTER(Epilogue), p, p,
+                                                   i64, i64, i64, i32, ctypes.POINTER(Tuning), p]
+            L.bsgemm_fp8_gemm_residual.restype = i32
+            f32, size = ctypes.c_float, ctypes.c_size_t
+            L.bsgemm_rms_norm_quantize_fp8.argtypes = [i32, i32, i32, p, p, p, f32, i64, i64, i32, p, p, p, p, p]
+            L.bsgemm_rms_norm_quantize_fp8.restype = i32
+            L.bsgemm_rms_norm_backward.argtypes = [i32, i32, p, p, p, p, p, i64, i64, p, p, p, size, p]
+            L.bsgemm_rms_norm_backward.restype = i32
+            L.bsgemm_rms_norm_backward_workspace.argtypes = [i64, i64]
+            L.bsgemm_rms_norm_backward_workspace.restype = size
+            L.bsgemm_activation_quantize_fp8.argtypes = [i32, i32, i32, p, i64, i64, i32, p, p, p]
+            L.bsgemm_activation_quantize_fp8.restype = i32
+            L.bsgemm_activation_backward_quantize_fp8.argtypes = [i32, i32, i32, p, p, i64, i64, i32, p, p, p, p,
+                                                                  size, p]
+            L.bsgemm_activation_backward_quantize_fp8.restype = i32
+            L.bsgemm_activation_backward_workspace.argtypes = [i64, i64, i32]
+            L.bsgemm_activation_backward_workspace.restype = size
             L.bsgemm_version.argtypes = []
             L.bsgemm_version.restype = i32
             _lib = L
@@ -188,14 +208,15 @@ def _format(x: torch.Tensor, given, name: str) -> int:
 
 
 def gemm(a, b, scale_a, scale_b, out=None, layout="nt", gran=128, tuning=None, stream=None,
-         a_format=None, b_format=None, bias=None, activation=None, out_dtype=torch.bfloat16):
+         a_format=None, b_format=None, bias=None, activation=None, out_dtype=torch.bfloat16, residual=None):
     """out[M,N] of the block-scaled FP8 GEMM; see ``include/bsgemm.h``.
 
     ``a_format`` / ``b_format``: "e4m3" or "e5m2"; taken from the tensor's
     dtype when it is a float8 type, E4M3 for uint8 codes unless given.
-    Fused epilogue: out = activation(acc + bias[n]) with ``bias`` an FP32 [N]
-    CUDA tensor or None, ``activation`` None / "relu" / "gelu" (erf form), and
-    ``out_dtype`` torch.bfloat16 or torch.float32."""
+    Fused epilogue: out = activation(acc + bias[n]) + residual with ``bias`` an
+    FP32 [N] CUDA tensor or None, ``activation`` None / "relu" / "gelu" (erf
+    form), ``out_dtype`` torch.bfloat16 or torch.float32, and ``residual`` an
+    [M, N] tensor of ``out_dtype`` or None; ``out`` may be ``residual`` itself."""
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
     fa = _format(a, a_format, "a")
@@ -220,14 +241,21 @@ def gemm(a, b, scale_a, scale_b, out=None, layout="nt", gran=128, tuning=None, s
     _device_tensor(out, "out", out_dtype, dev)
     if tuple(out.shape) != (M, N):
         raise ValueError(f"out must be a {out_dtype} [M, N] = [{M}, {N}] tensor, got {tuple(out.shape)}")
+    if residual is not None:
+        _device_tensor(residual, "residual", out_dtype, dev)
+        if tuple(residual.shape) != (M, N):
+            raise ValueError(f"residual must be [M, N] = [{M}, {N}], got {tuple(residual.shape)}")
     epi = None
     if bias is not None or ACTIVATIONS[activation] or out_dtype == torch.float32:
         epi = ctypes.byref(Epilogue(bias.data_ptr() if bias is not None else None, ACTIVATIONS[activation],
                                     1 if out_dtype == torch.float32 else 0))
     with torch.cuda.device(dev):
-        st = lib().bsgemm_fp8_gemm_fused(LAYOUTS[layout], fa, fb, a.data_ptr(), b.data_ptr(),
-                                         scale_a.data_ptr(), scale_b.data_ptr(), epi, out.data_ptr(), M,
-                                         N, K, int(gran), _tuning(tuning), _stream_handle(stream))
+        operands = (LAYOUTS[layout], fa, fb, a.data_ptr(), b.data_ptr(), scale_a.data_ptr(), scale_b.data_ptr(), epi)
+        sizes = (out.data_ptr(), M, N, K, int(gran), _tuning(tuning), _stream_handle(stream))
+        if residual is None:
+            st = lib().bsgemm_fp8_gemm_fused(*operands, *sizes)
+        else:
+            st = lib().bsgemm_fp8_gemm_residual(*operands, residual.data_ptr(), *sizes)
     if st != 0:
         raise BsgemmError(st, f"bsgemm {layout} M={M} N={N} K={K} g={gran}")
     return out
@@ -278,6 +306,207 @@ def quantize(x: torch.Tensor, gran: int = 128, fmt: str = "e4m3", q=None, scales
     if st != 0:
         raise BsgemmError(st, f"bsgemm_quantize_fp8 {rows}x{cols} g={gran}")
     return q, scales
+
+
+_SRC_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _matrix(t, name: str, dtype=None, device=None, shape=None):
+    """Check a dense 2-D FP32/BF16 CUDA matrix; returns it."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor")
+    if t.dtype not in _SRC_DTYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the first operand on {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _weight(t, name: str, cols: int, device):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _SRC_DTYPES:
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+    return _device_tensor(t, name, t.dtype, device, cols)
+
+
+class _OnStream:
+    """Makes ``device`` current and, where a stream is given, that stream too, so
+    that outputs and workspaces come from the memory of the stream that the
+    kernels run on. ``handle`` is that stream's."""
+
+    def __init__(self, device, stream):
+        self.contexts = []
+        if torch.cuda.current_device() != device.index:
+            self.contexts.append(torch.cuda.device(device))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.contexts.append(torch.cuda.stream(stream))
+        self.device = device
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        self.handle = torch.cuda.current_stream(self.device).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _codes_and_scales(rows, cols, gran, q, scales, device):
+    """The quantised outputs, allocated where the caller gave none."""
+    ok_g = gran in _GRANS
+    if q is None:
+        q = torch.empty((rows, cols), dtype=torch.uint8, device=device)
+    else:
+        _device_tensor(q, "q", torch.uint8, device, rows * cols)
+    if scales is None:
+        scales = torch.empty((_blocks(rows, gran), _blocks(cols, gran)) if ok_g else (1,), dtype=torch.float32,
+                             device=device)
+    else:
+        _device_tensor(scales, "scales", torch.float32, device,
+                       _blocks(rows, gran) * _blocks(cols, gran) if ok_g else None)
+    return q, scales
+
+
+def _given_activation(activation):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)}")
+    return ACTIVATIONS[activation]
+
+
+def rms_norm_quantize(x, weight, residual=None, eps=1e-6, gran=128, fmt="e4m3", return_rstd=False,
+                      residual_out=None, q=None, scales=None, stream=None):
+    """FP8 codes and block scales of the root-mean-square norm of x + residual.
+
+    ``x`` and ``residual`` (or None) are FP32 or BF16 [rows, cols]; ``weight``
+    is FP32 or BF16 [cols]. Returns (q, scales, h) or, with ``return_rstd``,
+    (q, scales, h, rstd): the GEMM's operand and scales as ``quantize`` gives
+    them, h = x + residual rounded to x's type (x itself without residual) and
+    the FP32 [rows] 1 / sqrt(mean(h^2) + eps), which ``rms_norm_backward``
+    takes. ``residual_out`` (h's buffer) may be ``x`` or ``residual``. See
+    ``bsgemm_rms_norm_quantize_fp8``."""
+    _matrix(x, "x")
+    dev, (rows, cols) = x.device, x.shape
+    weight = _weight(weight, "weight", cols, dev)
+    if fmt not in FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(FORMATS)}")
+    if residual is not None:
+        _matrix(residual, "residual", x.dtype, dev, x.shape)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual: without one the stream is x itself")
+    with _OnStream(dev, stream) as on:
+        q, scales = _codes_and_scales(rows, cols, gran, q, scales, dev)
+        if residual is not None:
+            residual_out = torch.empty_like(x) if residual_out is None else \
+                _matrix(residual_out, "residual_out", x.dtype, dev, x.shape)
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev) if return_rstd else None
+        st = lib().bsgemm_rms_norm_quantize_fp8(
+            _SRC_DTYPES[x.dtype], _SRC_DTYPES[weight.dtype], FORMATS[fmt], x.data_ptr(),
+            None if residual is None else residual.data_ptr(), weight.data_ptr(), float(eps), rows, cols, int(gran),
+            None if residual is None else residual_out.data_ptr(), q.data_ptr(), scales.data_ptr(),
+            None if rstd is None else rstd.data_ptr(), on.handle)
+    if st != 0:
+        raise BsgemmError(st, f"bsgemm_rms_norm_quantize_fp8 {rows}x{cols} g={gran}")
+    h = x if residual is None else residual_out
+    return (q, scales, h, rstd) if return_rstd else (q, scales, h)
+
+
+def rms_norm_backward(dy, h, weight, rstd, dresidual=None, dx=None, dweight=None, stream=None):
+    """Gradients of ``rms_norm_quantize`` (its quantiser passed straight through).
+
+    ``dy`` is the gradient of the normalised rows, ``h`` and ``rstd`` the
+    forward call's, ``dresidual`` the gradient that reaches h on the skip path
+    or None; all matrices of one type. Returns (dx, dweight): the gradient of x
+    and of the residual alike, and the FP32 [cols] gradient of the weight.
+    ``dx`` may be ``dy`` or ``dresidual``. See ``bsgemm_rms_norm_backward``."""
+    _matrix(dy, "dy")
+    dev, (rows, cols) = dy.device, dy.shape
+    _matrix(h, "h", dy.dtype, dev, dy.shape)
+    weight = _weight(weight, "weight", cols, dev)
+    _device_tensor(rstd, "rstd", torch.float32, dev, rows)
+    if dresidual is not None:
+        _matrix(dresidual, "dresidual", dy.dtype, dev, dy.shape)
+    L = lib()
+    with _OnStream(dev, stream) as on:
+        dx = torch.empty_like(dy) if dx is None else _matrix(dx, "dx", dy.dtype, dev, dy.shape)
+        if dweight is None:
+            dweight = torch.empty((cols,), dtype=torch.float32, device=dev)
+        else:
+            _device_tensor(dweight, "dweight", torch.float32, dev, cols)
+        nbytes = L.bsgemm_rms_norm_backward_workspace(rows, cols)
+        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        st = L.bsgemm_rms_norm_backward(
+            _SRC_DTYPES[dy.dtype], _SRC_DTYPES[weight.dtype], dy.data_ptr(), h.data_ptr(), weight.data_ptr(),
+            rstd.data_ptr(), None if dresidual is None else dresidual.data_ptr(), rows, cols, dx.data_ptr(),
+            dweight.data_ptr(), workspace.data_ptr(), nbytes, on.handle)
+    if st != 0:
+        raise BsgemmError(st, f"bsgemm_rms_norm_backward {rows}x{cols}")
+    return dx, dweight
+
+
+def activation_quantize(z, activation, gran=128, fmt="e4m3", q=None, scales=None, stream=None):
+    """FP8 codes and block scales of activation(z), z an FP32 or BF16 [rows, cols]
+    product with its bias; ``activation`` "relu" or "gelu" (without one,
+    ``quantize``). Returns (q, scales). See ``bsgemm_activation_quantize_fp8``."""
+    _matrix(z, "z")
+    act = _given_activation(activation)
+    if fmt not in FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(FORMATS)}")
+    dev, (rows, cols) = z.device, z.shape
+    with _OnStream(dev, stream) as on:
+        q, scales = _codes_and_scales(rows, cols, gran, q, scales, dev)
+        st = lib().bsgemm_activation_quantize_fp8(_SRC_DTYPES[z.dtype], FORMATS[fmt], act, z.data_ptr(), rows, cols,
+                                                  int(gran), q.data_ptr(), scales.data_ptr(), on.handle)
+    if st != 0:
+        raise BsgemmError(st, f"bsgemm_activation_quantize_fp8 {rows}x{cols} g={gran} {activation}")
+    return q, scales
+
+
+def activation_backward_quantize(dout, z, activation=None, gran=128, fmt="e4m3", bias_grad=True, q=None, scales=None,
+                                 dbias=None, stream=None):
+    """Gradient of the GEMM's epilogue: dz = dout * activation'(z) as codes and
+    scales, and the bias's gradient.
+
+    ``dout`` and ``z`` (the product with its bias; None where ``activation`` is
+    None or "none") are of one type. Returns (q, scales, dbias): one operand for
+    both gradient products, and the FP32 [cols] column sums of dz (None with
+    ``bias_grad=False``). See ``bsgemm_activation_backward_quantize_fp8``."""
+    _matrix(dout, "dout")
+    act = _given_activation(activation)
+    dev, (rows, cols) = dout.device, dout.shape
+    if (z is not None) != (act != 0):
+        raise ValueError("z is given with an activation, and only then")
+    if z is not None:
+        _matrix(z, "z", dout.dtype, dev, dout.shape)
+    if fmt not in FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(FORMATS)}")
+    if dbias is not None and not bias_grad:
+        raise ValueError("dbias is given but bias_grad is False")
+    L = lib()
+    with _OnStream(dev, stream) as on:
+        q, scales = _codes_and_scales(rows, cols, gran, q, scales, dev)
+        workspace, nbytes = None, 0
+        if bias_grad:
+            if dbias is None:
+                dbias = torch.empty((cols,), dtype=torch.float32, device=dev)
+            else:
+                _device_tensor(dbias, "dbias", torch.float32, dev, cols)
+            nbytes = L.bsgemm_activation_backward_workspace(rows, cols, int(gran))
+            if nbytes:
+                workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        st = L.bsgemm_activation_backward_quantize_fp8(
+            _SRC_DTYPES[dout.dtype], FORMATS[fmt], act, dout.data_ptr(), None if z is None else z.data_ptr(), rows,
+            cols, int(gran), q.data_ptr(), scales.data_ptr(), None if dbias is None else dbias.data_ptr(),
+            None if workspace is None else workspace.data_ptr(), nbytes, on.handle)
+    if st != 0:
+        raise BsgemmError(st, f"bsgemm_activation_backward_quantize_fp8 {rows}x{cols} g={gran} {activation}")
+    return q, scales, dbias
 
 
 def grouped_gemm(a, b, scale_a, scale_b, group_m, out=None, gran=128, a_format=None, b_format=None,

@@ -1,11 +1,12 @@
 """Build ``libbsgemm.so`` in-tree for sm_100a with nvcc.
 
 The C ABI unit (``csrc/bsgemm_api.cu``), the allocation-free entry point
-(``csrc/bsgemm_noalloc.cu``), the quantiser (``csrc/bsgemm_quant.cu``) and
-one kernel-instance unit per
-(granularity, layout) pair (``csrc/bsgemm_inst.cu`` compiled twelve times with
--DBSG_GRAN / -DBSG_LAYOUT) are compiled in parallel and linked into one shared
-library next to this file.  Objects are rebuilt only when a source under
+(``csrc/bsgemm_noalloc.cu``), the quantiser (``csrc/bsgemm_quant.cu``), the
+norm and activation kernels around the GEMM (``csrc/bsgemm_norm.cu``,
+``csrc/bsgemm_act.cu``) and two kernel-instance units per
+(granularity, layout) pair (``csrc/bsgemm_inst.cu`` compiled with
+-DBSG_GRAN / -DBSG_LAYOUT, with and without -DBSG_RES=1) are compiled in
+parallel and linked into one shared library next to this file.  Objects are rebuilt only when a source under
 ``csrc/`` or ``include/`` is newer than they are.
 
     python -m fp8_block_scaled_bsgemm_b200.build [--force] [-j N]
@@ -64,12 +65,18 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
     newest = _newest_source()
     units = [(os.path.join(CSRC, "bsgemm_api.cu"), os.path.join(BUILD, "bsgemm_api.o"), []),
              (os.path.join(CSRC, "bsgemm_noalloc.cu"), os.path.join(BUILD, "bsgemm_noalloc.o"), []),
-             (os.path.join(CSRC, "bsgemm_quant.cu"), os.path.join(BUILD, "bsgemm_quant.o"), [])]
+             (os.path.join(CSRC, "bsgemm_quant.cu"), os.path.join(BUILD, "bsgemm_quant.o"), []),
+             (os.path.join(CSRC, "bsgemm_norm.cu"), os.path.join(BUILD, "bsgemm_norm.o"), []),
+             (os.path.join(CSRC, "bsgemm_act.cu"), os.path.join(BUILD, "bsgemm_act.o"), [])]
     for g in GRANS:
         for lay in LAYOUTS:
             units.append((os.path.join(CSRC, "bsgemm_inst.cu"),
                           os.path.join(BUILD, f"bsgemm_inst_g{g}_{lay}.o"),
                           [f"-DBSG_GRAN={g}", f"-DBSG_LAYOUT={lay}"]))
+            # the instances that add a residual
+            units.append((os.path.join(CSRC, "bsgemm_inst.cu"),
+                          os.path.join(BUILD, f"bsgemm_inst_res_g{g}_{lay}.o"),
+                          [f"-DBSG_GRAN={g}", f"-DBSG_LAYOUT={lay}", "-DBSG_RES=1"]))
     todo = [u for u in units if force or not os.path.exists(u[1]) or os.path.getmtime(u[1]) < newest]
     if todo:
         jobs = jobs or max(1, min(len(todo), os.cpu_count() or 1))

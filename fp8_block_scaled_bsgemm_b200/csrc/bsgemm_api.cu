@@ -388,11 +388,12 @@ extern "C" bsgemm_status bsgemm_make_plan(int layout, int64_t M, int64_t N, int6
 }
 
 // ------------------------------------------------------------------ entry points
-extern "C" bsgemm_status bsgemm_fp8_gemm_fused(int layout, int a_format, int b_format, const void* a,
-                                               const void* b, const float* scale_a, const float* scale_b,
-                                               const bsgemm_epilogue* epi, void* out, int64_t M, int64_t N,
-                                               int64_t K, int gran, const bsgemm_tuning* tuning,
-                                               bsgemm_stream_t stream) {
+namespace {
+
+bsgemm_status gemm_call(int layout, int a_format, int b_format, const void* a, const void* b,
+                        const float* scale_a, const float* scale_b, const bsgemm_epilogue* epi,
+                        const void* residual, void* out, int64_t M, int64_t N, int64_t K, int gran,
+                        const bsgemm_tuning* tuning, bsgemm_stream_t stream) {
   if ((a_format != BSGEMM_FP8_E4M3 && a_format != BSGEMM_FP8_E5M2) ||
       (b_format != BSGEMM_FP8_E4M3 && b_format != BSGEMM_FP8_E5M2))
     return BSGEMM_ERR_INVALID_ARG;
@@ -408,6 +409,15 @@ extern "C" bsgemm_status bsgemm_fp8_gemm_fused(int layout, int a_format, int b_f
   }
   bsgemm_status st = check_args(layout, a, b, scale_a, scale_b, out, M, N, K, gran);
   if (st != BSGEMM_OK) return st;
+  if (residual) {
+    if (!aligned(residual, 16)) return BSGEMM_ERR_MISALIGNED;
+    // the residual may be out itself, but not a shifted part of it: an element
+    // must be read by the warp that overwrites it
+    const uintptr_t r = reinterpret_cast<uintptr_t>(residual), o = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t bytes = static_cast<uintptr_t>(M) * N * ((opts.epi & bsg::kEpiOutF32) ? 4 : 2);
+    if (r != o && r < o + bytes && o < r + bytes) return BSGEMM_ERR_INVALID_ARG;
+    opts.residual = residual;
+  }
   DeviceInfo dev;
   st = device_info(dev);
   if (st != BSGEMM_OK) return st;
@@ -416,7 +426,9 @@ extern "C" bsgemm_status bsgemm_fp8_gemm_fused(int layout, int a_format, int b_f
   if (st != BSGEMM_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
-#define BSG_RUN(G, L) bsg_host::run_g##G##_##L(pl, a, b, scale_a, scale_b, out, m, n, k, opts, s, dev)
+#define BSG_RUN(G, L)                                                                            \
+  (residual ? bsg_host::run_res_g##G##_##L(pl, a, b, scale_a, scale_b, out, m, n, k, opts, s, dev) \
+            : bsg_host::run_g##G##_##L(pl, a, b, scale_a, scale_b, out, m, n, k, opts, s, dev))
 #define BSG_RUN_LAYOUTS(G)                              \
   switch (layout) {                                     \
     case BSGEMM_LAYOUT_NT: return BSG_RUN(G, nt);       \
@@ -431,6 +443,27 @@ extern "C" bsgemm_status bsgemm_fp8_gemm_fused(int layout, int a_format, int b_f
   }
 #undef BSG_RUN_LAYOUTS
 #undef BSG_RUN
+}
+
+}  // namespace
+
+extern "C" bsgemm_status bsgemm_fp8_gemm_fused(int layout, int a_format, int b_format, const void* a,
+                                               const void* b, const float* scale_a, const float* scale_b,
+                                               const bsgemm_epilogue* epi, void* out, int64_t M, int64_t N,
+                                               int64_t K, int gran, const bsgemm_tuning* tuning,
+                                               bsgemm_stream_t stream) {
+  return gemm_call(layout, a_format, b_format, a, b, scale_a, scale_b, epi, nullptr, out, M, N, K, gran,
+                   tuning, stream);
+}
+
+extern "C" bsgemm_status bsgemm_fp8_gemm_residual(int layout, int a_format, int b_format, const void* a,
+                                                  const void* b, const float* scale_a, const float* scale_b,
+                                                  const bsgemm_epilogue* epi, const void* residual, void* out,
+                                                  int64_t M, int64_t N, int64_t K, int gran,
+                                                  const bsgemm_tuning* tuning, bsgemm_stream_t stream) {
+  if (!residual) return BSGEMM_ERR_INVALID_ARG;
+  return gemm_call(layout, a_format, b_format, a, b, scale_a, scale_b, epi, residual, out, M, N, K, gran,
+                   tuning, stream);
 }
 
 extern "C" bsgemm_status bsgemm_fp8_grouped_nt(int a_format, int b_format, const void* a, const void* b,

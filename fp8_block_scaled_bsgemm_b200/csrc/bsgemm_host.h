@@ -35,6 +35,9 @@ class PerDeviceOnce {
   std::atomic<uint64_t> bits_{0};
 };
 
+// The current device (looked up once per device); an error unless it is sm_100.
+bsgemm_status device_info(DeviceInfo& out);
+
 struct Workspace {
   float* ws = nullptr;
   size_t ws_bytes = 0;
@@ -71,6 +74,7 @@ struct CallOpts {
   int a_fmt = BSGEMM_FP8_E4M3;   // bsgemm_fp8_format of the logical A operand
   int b_fmt = BSGEMM_FP8_E4M3;   // ... and of B
   const float* bias = nullptr;   // FP32 [N] or null
+  const void* residual = nullptr; // [M, N] of the output's type, or null (run_res_* alone take one)
   int epi = 0;                   // activation (bits 0-1) | FP32 output (bit 2)
   const int* group_m = nullptr;  // grouped GEMM: device rows per group
   int num_groups = 0;
@@ -79,7 +83,11 @@ struct CallOpts {
 #define BSG_RUN_DECL(G, L)                                                                       \
   bsgemm_status run_g##G##_##L(const bsgemm_plan& plan, const void* a, const void* b,          \
                                const float* sa, const float* sb, void* out, int M, int N, int K, \
-                               const CallOpts& opts, cudaStream_t stream, const DeviceInfo& dev);
+                               const CallOpts& opts, cudaStream_t stream, const DeviceInfo& dev); \
+  bsgemm_status run_res_g##G##_##L(const bsgemm_plan& plan, const void* a, const void* b,      \
+                                   const float* sa, const float* sb, void* out, int M, int N,   \
+                                   int K, const CallOpts& opts, cudaStream_t stream,            \
+                                   const DeviceInfo& dev);
 BSG_RUN_DECL(64, nt) BSG_RUN_DECL(64, tn) BSG_RUN_DECL(64, nn) BSG_RUN_DECL(64, tt)
 BSG_RUN_DECL(128, nt) BSG_RUN_DECL(128, tn) BSG_RUN_DECL(128, nn) BSG_RUN_DECL(128, tt)
 BSG_RUN_DECL(256, nt) BSG_RUN_DECL(256, tn) BSG_RUN_DECL(256, nn) BSG_RUN_DECL(256, tt)

@@ -1,6 +1,7 @@
 // Kernel instances and launch code for one (granularity, layout) pair.
-// The build compiles this file once per pair with -DBSG_GRAN=<64|128|256>
-// and -DBSG_LAYOUT=<nt|tn|nn|tt>, so the twelve pairs build in parallel.
+// The build compiles this file twice per pair with -DBSG_GRAN=<64|128|256>
+// and -DBSG_LAYOUT=<nt|tn|nn|tt>, the second time with -DBSG_RES=1 for the
+// instances that add a residual, so the twenty-four units build in parallel.
 #include <cstring>
 
 #include "bsgemm_host.h"
@@ -14,8 +15,16 @@
 #error "compile with -DBSG_LAYOUT=nt|tn|nn|tt"
 #endif
 
+#ifndef BSG_RES
+#define BSG_RES 0
+#endif
+
 #define BSG_CAT2(a, b, c, d) a##b##_##c
+#if BSG_RES
+#define BSG_RUN_NAME(G, L) BSG_CAT2(run_res_g, G, L, )
+#else
 #define BSG_RUN_NAME(G, L) BSG_CAT2(run_g, G, L, )
+#endif
 #define BSG_STR2(x) #x
 #define BSG_STR(x) BSG_STR2(x)
 
@@ -26,6 +35,7 @@ namespace {
 constexpr const char* kLayout = BSG_STR(BSG_LAYOUT);
 constexpr bool kAMn = kLayout[0] == 't';
 constexpr bool kBMn = kLayout[1] == 'n';
+constexpr bool kRes = BSG_RES != 0;
 
 // Format fields of the instruction descriptor for operands P (MMA A side)
 // and Q (MMA B side).
@@ -38,7 +48,7 @@ bsgemm_status launch(const bsgemm_plan& plan, const void* a, const void* b, cons
                      const float* sb, void* out, int M, int N, int K, const CallOpts& opts,
                      cudaStream_t stream, const DeviceInfo& dev) {
   using SC = bsg::StageCfg<BNQ, Q_MN, SWAP, GROUPED>;
-  auto kern = bsg::bsgemm_kernel<BNQ, GRAN, SWAP, P_MN, Q_MN, SPLIT, GROUPED>;
+  auto kern = bsg::bsgemm_kernel<BNQ, GRAN, SWAP, P_MN, Q_MN, SPLIT, GROUPED, kRes>;
 
   // P/Q operands: normally P = A (M rows), Q = B (N rows); swapped P = B, Q = A
   const void* p_ptr = SWAP ? b : a;
@@ -79,6 +89,7 @@ bsgemm_status launch(const bsgemm_plan& plan, const void* a, const void* b, cons
   prm.fmt_bits = SWAP ? fmt_bits(opts.b_fmt, opts.a_fmt) : fmt_bits(opts.a_fmt, opts.b_fmt);
   prm.epi = opts.epi;
   prm.bias = opts.bias;
+  prm.residual = opts.residual;
   prm.group_m = opts.group_m;
   prm.num_groups = GROUPED ? opts.num_groups : 0;
   prm.sP = SWAP ? sb : sa;
@@ -132,7 +143,7 @@ bsgemm_status launch_pair(const bsgemm_plan& plan, const void* a, const void* b,
                           const float* sb, void* out, int M, int N, int K, const CallOpts& opts,
                           cudaStream_t stream, const DeviceInfo& dev) {
   using PC = bsg::PairCfg;
-  auto kern = bsg::bsgemm_pair_kernel<GRAN, P_MN, Q_MN>;
+  auto kern = bsg::bsgemm_pair_kernel<GRAN, P_MN, Q_MN, kRes>;
   CUtensorMap tm_p, tm_q;
   bool ok = true;
   if (P_MN) ok &= make_map_2d(&tm_p, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, M, K, M, 128, bsg::BK);
@@ -157,6 +168,7 @@ bsgemm_status launch_pair(const bsgemm_plan& plan, const void* a, const void* b,
   prm.fmt_bits = fmt_bits(opts.a_fmt, opts.b_fmt);
   prm.epi = opts.epi;
   prm.bias = opts.bias;
+  prm.residual = opts.residual;
   prm.sP = sa;
   prm.sQ = sb;
   prm.out = static_cast<__nv_bfloat16*>(out);
@@ -217,8 +229,8 @@ bsgemm_status BSG_RUN_NAME(BSG_GRAN, BSG_LAYOUT)(const bsgemm_plan& pl, const vo
                                                  const DeviceInfo& d) {
   constexpr int G = BSG_GRAN;
   if (pl.grouped) {
-    // grouped GEMM: NT only, whole tiles
-    if constexpr (!kAMn && !kBMn) {
+    // grouped GEMM: NT only, whole tiles, no residual
+    if constexpr (!kAMn && !kBMn && !kRes) {
       if (pl.bnq == 128) return launch<128, G, false, false, false, false, true>(pl, a, b, sa, sb, out, M, N, K, o, s, d);
       return launch<256, G, false, false, false, false, true>(pl, a, b, sa, sb, out, M, N, K, o, s, d);
     } else {

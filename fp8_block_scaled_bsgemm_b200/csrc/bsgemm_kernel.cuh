@@ -95,6 +95,7 @@ struct Params {
   int epi;               // epilogue: activation (bits 0-1: 0 none, 1 ReLU, 2 GELU), bit 2 FP32 output
   int num_groups;        // grouped GEMM: number of groups (0 otherwise)
   const float* bias;     // FP32 [N] added before the activation, or null
+  const void* residual;  // [M][N] in out's type, added after the activation (RES instances; may be out itself)
   const int* group_m;    // grouped GEMM: rows of each group (device, num_groups entries)
   const float* sP;       // [Pb][Kb]
   const float* sQ;       // [Qb][Kb]
@@ -493,6 +494,86 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t
                : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// acc += residual on the rows and columns of store_tile_tma (which follows).
+// A lane owns a row, and rows lie far apart, so the warp reads each chunk of
+// 32 rows x 128 bytes in memory order (8 lanes to a row's 128 bytes, four rows
+// to an instruction) and turns it through its staging buffer, in the same
+// swizzled places as the store. The loads go to L2 (ld.global.cg): out may be
+// the residual's own buffer. Every element is read by the warp that writes it,
+// before it writes it.
+template <int NP>
+__device__ __forceinline__ void add_residual(const Params& p, uint32_t buf, int m0, int n0, float2 (&acc)[NP],
+                                             uint32_t lane) {
+  if (m0 >= p.M) return;  // the warp's rows are all past the end
+  const uint32_t own = buf + lane * 128, sw = lane & 7;
+  const uint32_t piece = lane & 7;
+  auto chunks = [&](auto f32_tag) {
+    constexpr bool kF32 = decltype(f32_tag)::value != 0;
+    constexpr int kCols = kF32 ? 32 : 64;           // columns per chunk
+    constexpr int kChunks = 2 * NP / kCols;
+    constexpr size_t kElem = kF32 ? 4 : 2;
+    auto load = [&](int c, uint4 (&v)[8]) {
+      const int n = n0 + c * kCols + static_cast<int>(piece) * (kCols / 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int m = m0 + 4 * i + static_cast<int>(lane >> 3);
+        v[i] = make_uint4(0, 0, 0, 0);
+        // N % 8 == 0: a 16-byte piece lies wholly inside the row or past it
+        if (m < p.M && n < p.N)
+          v[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.residual) +
+                                                       (static_cast<size_t>(m) * p.N + n) * kElem));
+      }
+    };
+    uint4 cur[8], nxt[8];
+    load(0, cur);
+    // the previous tile's store must have finished reading the buffer
+    if (lane == 0) bulk_wait_group_read0();
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      if (c + 1 < kChunks) load(c + 1, nxt);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t r = 4 * i + (lane >> 3);
+        st_shared_v4(buf + r * 128 + ((piece ^ (r & 7)) << 4), cur[i].x, cur[i].y, cur[i].z, cur[i].w);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint4 v = ld_shared_v4(own + ((u ^ sw) << 4));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (kF32) {
+          const int i = c * 16 + 2 * u;
+          acc[i].x += __uint_as_float(w[0]);
+          acc[i].y += __uint_as_float(w[1]);
+          acc[i + 1].x += __uint_as_float(w[2]);
+          acc[i + 1].y += __uint_as_float(w[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc[c * 32 + 4 * u + k].x += __uint_as_float(w[k] << 16);
+            acc[c * 32 + 4 * u + k].y += __uint_as_float(w[k] & 0xFFFF0000u);
+          }
+        }
+      }
+      __syncwarp();   // every row is read before the next chunk, or the store, is written over it
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cur[i] = nxt[i];
+    }
+  };
+  if (p.epi & kEpiOutF32) chunks(ActTag<1>{});
+  else                    chunks(ActTag<0>{});
+}
+
 // TMA-store epilogue of one promotion warp: lane l holds row m0 + l, columns
 // [n0, n0 + 2 * NP) (acc pairs in column order, epilogue already applied).
 // The warp's rows go out in chunks of 128 bytes per row (64 BF16 or 32 FP32
@@ -586,7 +667,9 @@ __device__ __forceinline__ void store_row_run(const Params& p, int m, int n0, fl
 }
 
 // ---------------------------------------------------------------- kernel
-template <int BNQ, int GRAN, bool SWAP, bool P_MN, bool Q_MN, bool SPLIT, bool GROUPED = false>
+// RES: the instance adds Params.residual (instances apart, so that the others
+// carry none of its code or registers).
+template <int BNQ, int GRAN, bool SWAP, bool P_MN, bool Q_MN, bool SPLIT, bool GROUPED = false, bool RES = false>
 __global__ void __launch_bounds__(kNumThreads, 1)
     bsgemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_out, const Params p) {
@@ -1110,6 +1193,25 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       if constexpr (SWAP) {
         // tile rows are N, tile columns are M: out[m][n]
         const int n = w.tp * BM + row_in_tile;
+        // the residual's elements of this thread, column n of rows m0 ..: a
+        // warp reads 32 consecutive n of a row at a time
+        float res[RES ? kHalf : 1];
+        if constexpr (RES) {
+          const int m0 = w.tq * BNQ + half * kHalf;
+          const size_t at = static_cast<size_t>(m0) * p.N + n;
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) {
+            res[i] = 0.f;
+            if (m0 + i < p.M && n < p.N) {
+              const size_t e = at + static_cast<size_t>(i) * p.N;
+              if (p.epi & kEpiOutF32)
+                res[i] = __ldcg(static_cast<const float*>(p.residual) + e);
+              else
+                res[i] = __uint_as_float(
+                    static_cast<uint32_t>(__ldcg(static_cast<const unsigned short*>(p.residual) + e)) << 16);
+            }
+          }
+        }
         if (!(p.epi & kEpiOutF32)) {
           // BF16: the whole tile goes through the staging buffer, [BNQ][128]
           // in the output's order: for each m, the warp's 32 lanes write 32
@@ -1122,7 +1224,16 @@ __global__ void __launch_bounds__(kNumThreads, 1)
           if (ew == 0 && lane == 0) bulk_wait_group_read0();
           named_barrier_sync(2, kNumEpiThreads);
           const uint32_t col0 = stage + (half * kHalf * BM + row_in_tile) * 2;  // m = half * kHalf
-          if (p.bias == nullptr && act == 0) {
+          if constexpr (RES) {
+            with_act(act, [&](auto tag) {
+              constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+              for (int i = 0; i < kHalf; ++i) {
+                const float v = epi_act_t<ACT>(((i & 1) ? acc[i / 2].y : acc[i / 2].x) + bn) + res[i];
+                st_shared_b16(col0 + i * BM * 2, __bfloat16_as_ushort(__float2bfloat16_rn(v)));
+              }
+            });
+          } else if (p.bias == nullptr && act == 0) {
             // the plain BF16 output: no activation code in the loop (evaluated
             // per element, the erf branch cost ~90 cycles a value)
 #pragma unroll
@@ -1155,7 +1266,8 @@ __global__ void __launch_bounds__(kNumThreads, 1)
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) {
               const int m = w.tq * BNQ + half * kHalf + i;
-              const float v = epi_act_t<ACT>(((i & 1) ? acc[i / 2].y : acc[i / 2].x) + bn);
+              float v = epi_act_t<ACT>(((i & 1) ? acc[i / 2].y : acc[i / 2].x) + bn);
+              if constexpr (RES) v += res[i];
               if (m < p.M) reinterpret_cast<float*>(p.out)[static_cast<size_t>(m) * p.N + n] = v;
             }
           });
@@ -1165,6 +1277,8 @@ __global__ void __launch_bounds__(kNumThreads, 1)
         // stores its 32 rows through its staging buffer
         const int n0 = w.tq * BNQ + half * kHalf;
         apply_epi<kHalf / 2>(p, n0, acc);
+        if constexpr (RES)
+          add_residual<kHalf / 2>(p, smem_addr(epi_bufs + ew * kEpiChunkBytes), w.tp * BM + quad * 32, n0, acc, lane);
         store_tile_tma<kHalf / 2>(p, &tm_out, smem_addr(epi_bufs + ew * kEpiChunkBytes),
                                   w.tp * BM + quad * 32, n0, acc, lane);
       } else {

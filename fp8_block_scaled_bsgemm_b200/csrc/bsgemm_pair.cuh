@@ -58,7 +58,8 @@ __device__ __forceinline__ constexpr uint32_t instr_desc_pair() {
 
 // Whole 256 x 256 tiles only (no split-K / stream-K); Params.tiles_p and
 // tiles_q count pair tiles, Params.num_work is their number.
-template <int GRAN, bool P_MN, bool Q_MN>
+// RES: the instance adds Params.residual, as in bsgemm_kernel.
+template <int GRAN, bool P_MN, bool Q_MN, bool RES = false>
 __global__ void __launch_bounds__(kNumThreads, 1)
     bsgemm_pair_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_out, const Params p) {
@@ -368,6 +369,8 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       // the warp stores its 32 rows through its staging buffer
       const int n0 = tq * kPairN + half * kHalf;
       apply_epi<kHalf / 2>(p, n0, acc);
+      if constexpr (RES)
+        add_residual<kHalf / 2>(p, smem_addr(epi_bufs + ew * kEpiChunkBytes), prow0 + quad * 32, n0, acc, lane);
       store_tile_tma<kHalf / 2>(p, &tm_out, smem_addr(epi_bufs + ew * kEpiChunkBytes), prow0 + quad * 32, n0,
                                 acc, lane);
     }

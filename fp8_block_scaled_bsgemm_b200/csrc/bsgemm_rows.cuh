@@ -1,0 +1,224 @@
+// Pieces shared by the row-wise kernels around the GEMM (bsgemm_norm.cu,
+// bsgemm_act.cu): runs of 8 consecutive columns, packed FP32 arithmetic and
+// the FP8 encoding.
+//
+// All of these kernels move far more bytes than they compute, so a thread's
+// unit of work is a run: 16 bytes of BF16 or 32 bytes of FP32, loaded and
+// stored as 16-byte words; 8 codes are stored as one 8-byte word. Rows are
+// multiples of 16 columns, so a run lies wholly inside the matrix or outside.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "bsgemm.h"
+#include "ptx.cuh"
+
+namespace bsgr {
+
+constexpr int kVec = 8;  // columns per run
+
+// A run as it lies in memory; widened to FP32 on use (a BF16 run held this
+// way costs 4 registers rather than 8).
+template <bool BF16>
+struct Run {
+  uint4 w[BF16 ? 1 : 2];
+};
+
+template <bool BF16>
+__device__ __forceinline__ Run<BF16> zero_run() {
+  Run<BF16> r;
+#pragma unroll
+  for (int h = 0; h < (BF16 ? 1 : 2); ++h) r.w[h] = make_uint4(0, 0, 0, 0);
+  return r;
+}
+
+// Loads go through L2 only (ld.global.cg): each run is read once per pass, and
+// where an output may be the same buffer as an input no stale line can stay
+// in L1.
+template <bool BF16>
+__device__ __forceinline__ Run<BF16> load_run(const void* base, int64_t elem) {
+  Run<BF16> r;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + elem * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int h = 0; h < (BF16 ? 1 : 2); ++h) r.w[h] = __ldcg(p + h);
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_run(void* base, int64_t elem, const Run<BF16>& r) {
+  uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + elem * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int h = 0; h < (BF16 ? 1 : 2); ++h) p[h] = r.w[h];
+}
+
+// The run's columns as four FP32 pairs (exact).
+template <bool BF16>
+__device__ __forceinline__ void widen(const Run<BF16>& r, float2 (&v)[4]) {
+  if constexpr (BF16) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v[2 * h] = make_float2(__uint_as_float(r.w[h].x), __uint_as_float(r.w[h].y));
+      v[2 * h + 1] = make_float2(__uint_as_float(r.w[h].z), __uint_as_float(r.w[h].w));
+    }
+  }
+}
+
+// Four FP32 pairs as a run of the type: one rounding to nearest even for BF16.
+template <bool BF16>
+__device__ __forceinline__ Run<BF16> narrow(const float2 (&v)[4]) {
+  Run<BF16> r;
+  if constexpr (BF16) {
+    r.w[0] = make_uint4(bsg::pack_bf16x2(v[0].x, v[0].y), bsg::pack_bf16x2(v[1].x, v[1].y),
+                        bsg::pack_bf16x2(v[2].x, v[2].y), bsg::pack_bf16x2(v[3].x, v[3].y));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      r.w[h] = make_uint4(__float_as_uint(v[2 * h].x), __float_as_uint(v[2 * h].y),
+                          __float_as_uint(v[2 * h + 1].x), __float_as_uint(v[2 * h + 1].y));
+  }
+  return r;
+}
+
+// Pairwise FP32 arithmetic, one instruction per pair, each element rounded once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <int FMT>
+constexpr float kFmax = FMT == BSGEMM_FP8_E5M2 ? 57344.0f : 448.0f;
+
+// A block's scale: amax / FMAX, or 1 where that is 0 (an empty block, or one
+// whose amax / FMAX is below the smallest FP32 value).
+template <int FMT>
+__device__ __forceinline__ float block_scale(float amax) {
+  const float s = __fdiv_rn(amax, kFmax<FMT>);
+  return s > 0.f ? s : 1.f;
+}
+
+// FP8 codes of a (low byte) and b: round to nearest even, saturating.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode2(float2 v) {
+  return static_cast<uint32_t>(
+      __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, FMT == BSGEMM_FP8_E5M2 ? __NV_E5M2 : __NV_E4M3));
+}
+
+// Stores the codes of v / s. The quotient is v times the rounded reciprocal of
+// s: within 1.5 units of FP32's last place of the divided value, which is
+// itself that far from the exact one, against a code's half step of 2^-4. A
+// scale whose reciprocal could overflow takes the division.
+constexpr float kRcpMinScale = 0x1p-100f;
+
+template <int FMT>
+__device__ __forceinline__ void store_codes(uint8_t* q, int64_t elem, const float2 (&v)[4], float s, float rs) {
+  uint32_t c[4];
+  if (s >= kRcpMinScale) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = encode2<FMT>(mul2(v[i], both(rs)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = encode2<FMT>(make_float2(__fdiv_rn(v[i].x, s), __fdiv_rn(v[i].y, s)));
+  }
+  *reinterpret_cast<uint2*>(q + elem) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// Larger of a and the run's magnitudes; NaNs are passed over.
+__device__ __forceinline__ float max_abs(float a, const float2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+  return a;
+}
+
+// Store a float to a CTA's shared memory in the cluster (a shared::cluster address).
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// ------------------------------------------------------------------ host side
+
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// Sizes, types and device of a row-wise call; nothing is launched on an error.
+inline bsgemm_status check_rows(int src_dtype, int64_t rows, int64_t cols) {
+  if (src_dtype != BSGEMM_SRC_F32 && src_dtype != BSGEMM_SRC_BF16) return BSGEMM_ERR_INVALID_ARG;
+  if (rows <= 0 || cols <= 0 || rows > (1 << 30) || cols > (1 << 30)) return BSGEMM_ERR_INVALID_ARG;
+  return cols % 16 ? BSGEMM_ERR_MISALIGNED : BSGEMM_OK;
+}
+
+// A buffer of a call, for the check of overlaps.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+// True where an output shares memory with another output or with an input.
+template <int NO, int NI>
+bool any_overlap(const Span (&out)[NO], const Span (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = i + 1; j < NO; ++j)
+      if (overlap(out[i], out[j])) return true;
+    for (int j = 0; j < NI; ++j)
+      if (overlap(out[i], in[j])) return true;
+  }
+  return false;
+}
+// `b`, or no buffer where it is the very buffer `a` (allowed where a call says so).
+inline Span unless_same(const Span& a, const Span& b) { return a.p == b.p ? Span{nullptr, 0} : b; }
+
+inline size_t blocks_bytes(int64_t rows, int64_t cols, int g) {
+  return static_cast<size_t>((rows + g - 1) / g) * static_cast<size_t>((cols + g - 1) / g) * sizeof(float);
+}
+
+// Adds up `parts` rows of partial sums in order: out[c] = sum_i part[i][c].
+bsgemm_status launch_column_sum(const float* part, int parts, int64_t cols, float* out, cudaStream_t stream);
+
+// A launch that may overlap its set-up with the end of the stream's previous
+// kernel (every kernel here waits for it before touching global memory).
+template <typename... A, typename... B>
+bsgemm_status launch_rows(void (*kern)(A...), int64_t grid, int threads, size_t smem, int cluster,
+                          cudaStream_t stream, B... args) {
+  if (grid < 1 || grid > 0x7FFFFFFFll) return BSGEMM_ERR_INVALID_ARG;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return BSGEMM_ERR_CUDA;
+  }
+  return BSGEMM_OK;
+}
+
+}  // namespace bsgr

@@ -79,6 +79,7 @@
 #ifndef BSGEMM_H
 #define BSGEMM_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -255,6 +256,111 @@ bsgemm_status bsgemm_fp8_gemm_fused(int layout, int a_format, int b_format, cons
                                     const bsgemm_epilogue *epi, void *out, int64_t M, int64_t N,
                                     int64_t K, int gran, const bsgemm_tuning *tuning,
                                     bsgemm_stream_t stream);
+
+/* bsgemm_fp8_gemm_fused that also adds a residual, after the activation:
+ *   out[m,n] = act(acc[m,n] + bias[n]) + residual[m,n]
+ * residual is [M,N] row-major in out's type (epi's out_dtype, BF16 without
+ * epi), 16-byte aligned. The sum is taken in FP32 and rounded once. residual
+ * may be out itself (the residual stream updated in place); any other overlap
+ * of the two is BSGEMM_ERR_INVALID_ARG, and so is a NULL residual. With split-K
+ * or stream-K the residual is added once, after the pieces are summed.
+ * Everything else as bsgemm_fp8_gemm_fused. Gradients: the residual's is that
+ * of out; the rest is bsgemm_activation_backward_quantize_fp8 below and the
+ * GEMM itself. */
+bsgemm_status bsgemm_fp8_gemm_residual(int layout, int a_format, int b_format, const void *a,
+                                       const void *b, const float *scale_a, const float *scale_b,
+                                       const bsgemm_epilogue *epi, const void *residual, void *out,
+                                       int64_t M, int64_t N, int64_t K, int gran,
+                                       const bsgemm_tuning *tuning, bsgemm_stream_t stream);
+
+/* ---- norm, activation and their gradients ---------------------------------
+ * The steps between two GEMMs of a transformer sublayer, each fused with the
+ * quantisation of its result into the next GEMM's operand. Shared rules:
+ *   - matrices are dense row-major [rows, cols], rows, cols in 1 .. 2^30,
+ *     cols % 16 == 0 (else BSGEMM_ERR_MISALIGNED), of src_dtype (FP32 or BF16;
+ *     one type for all of a call's matrices), device pointers 16-byte aligned;
+ *   - q, scales, gran and fp8_format are the quantiser's (above), except that
+ *     a block whose amax / FMAX rounds to 0 also gets scale 1. Values are
+ *     quantised as computed in FP32, without a rounding to src_dtype between;
+ *   - sums, statistics and gradients of vectors are FP32, added in a fixed
+ *     order: the same inputs give bit-identical outputs;
+ *   - inputs must be finite. A NaN or infinity spoils the codes of its row
+ *     (norm) or of itself (activation) and may make its blocks' scales and
+ *     the sums over it infinite or NaN; nothing else is affected;
+ *   - errors are found before any launch; nothing is written then. Unknown
+ *     types, formats or activations, NULL where a pointer is needed:
+ *     BSGEMM_ERR_INVALID_ARG. gran: BSGEMM_ERR_UNSUPPORTED_GRAN;
+ *   - outputs share no memory with inputs or with each other, except where an
+ *     output may be an input itself; otherwise BSGEMM_ERR_INVALID_ARG;
+ *   - workspaces are the caller's: device memory of at least the bytes that the
+ *     size function gives (it touches no device), for this call alone until
+ *     the stream has passed it. Nothing in them is kept, and the library
+ *     allocates none, so these calls can be captured into graphs, and two
+ *     graphs share scratch only if their caller gives both the same.
+ * Like the GEMM, the kernels use programmatic dependent launch and wait for
+ * the stream's earlier kernels before they touch memory. */
+
+/* h = x + residual (FP32, rounded to src_dtype; h = x without residual),
+ * rstd = 1 / sqrt(mean over the row of h^2 + eps), y = h * rstd * weight, and
+ * q, scales of y.
+ *   residual, residual_out  both or neither (NULL); residual_out [rows, cols]
+ *                receives h and may be x or residual itself. It is the rounded
+ *                h that is normalised, as the next layer and the backward pass
+ *                read it.
+ *   weight       [cols] of weight_dtype (bsgemm_src_dtype)
+ *   eps          finite, > 0
+ *   rstd         FP32 [rows], or NULL: kept for the backward pass
+ * A row of values past 2^56 in magnitude may overflow its sum of squares
+ * (rstd is then 0, and so is y). */
+bsgemm_status bsgemm_rms_norm_quantize_fp8(int src_dtype, int weight_dtype, int fp8_format,
+                                           const void *x, const void *residual,
+                                           const void *weight, float eps, int64_t rows,
+                                           int64_t cols, int gran, void *residual_out, void *q,
+                                           float *scales, float *rstd, bsgemm_stream_t stream);
+
+/* The gradient of y = h * rstd * weight, from dy [rows, cols]; the quantiser
+ * is passed straight through. With n = h * rstd and dn = dy * weight:
+ *   dx = rstd * (dn - n * mean over the row of dn * n) + dresidual
+ *   dweight[c] = sum over rows of dy * n                       (FP32 [cols])
+ *   h, rstd    the forward call's (h is x where there was no residual)
+ *   dresidual  [rows, cols], the gradient that reaches h on the skip path, or
+ *              NULL
+ *   dx         [rows, cols], the gradient of x and of the residual alike; may
+ *              be dy or dresidual itself
+ * dweight and workspace 16-byte aligned; cols <= 65536, and a workspace smaller
+ * than bsgemm_rms_norm_backward_workspace is BSGEMM_ERR_INVALID_ARG. */
+size_t bsgemm_rms_norm_backward_workspace(int64_t rows, int64_t cols);
+bsgemm_status bsgemm_rms_norm_backward(int src_dtype, int weight_dtype, const void *dy,
+                                       const void *h, const void *weight, const float *rstd,
+                                       const void *dresidual, int64_t rows, int64_t cols, void *dx,
+                                       float *dweight, void *workspace, size_t workspace_bytes,
+                                       bsgemm_stream_t stream);
+
+/* q, scales of act(z): the next GEMM's operand from the product z (bias
+ * included) as a GEMM stored it. z is left as it is, for the backward pass.
+ * activation: ReLU or GELU as in the epilogue (NONE is bsgemm_quantize_fp8:
+ * BSGEMM_ERR_INVALID_ARG here). */
+bsgemm_status bsgemm_activation_quantize_fp8(int src_dtype, int fp8_format, int activation,
+                                             const void *z, int64_t rows, int64_t cols, int gran,
+                                             void *q, float *scales, bsgemm_stream_t stream);
+
+/* The gradient of the epilogue out = act(z) [+ residual], z = acc + bias[n]:
+ *   dz = dout * act'(z)                       as q, scales (one set serves both
+ *                                             gradient products: the g x g blocks
+ *                                             are the same read transposed)
+ *   dbias[n] = sum over rows of dz            (FP32 [cols], or NULL)
+ * act' is 0 at 0 for ReLU, Phi(z) + z phi(z) for GELU, 1 for NONE (z is then
+ * NULL, and only then). workspace: at least
+ * bsgemm_activation_backward_workspace bytes where dbias is given, else unused;
+ * a smaller one is BSGEMM_ERR_INVALID_ARG. */
+size_t bsgemm_activation_backward_workspace(int64_t rows, int64_t cols, int gran);
+bsgemm_status bsgemm_activation_backward_quantize_fp8(int src_dtype, int fp8_format,
+                                                      int activation, const void *dout,
+                                                      const void *z, int64_t rows, int64_t cols,
+                                                      int gran, void *q, float *scales,
+                                                      float *dbias, void *workspace,
+                                                      size_t workspace_bytes,
+                                                      bsgemm_stream_t stream);
 
 /* ---- grouped GEMM ---------------------------------------------------------
  * Many independent NT products in one persistent launch, the pages' "batch
