@@ -222,13 +222,12 @@ __global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const __grid_co
       if (tid % L == 0) atomicMax(&block_max[buf][slot], __float_as_uint(amax));
     }
     __syncthreads();
-    const float s = block_scale<FMT>(__uint_as_float(block_max[buf][slot]));
-    const float rcp = __frcp_rn(s);
+    const Scale s = block_scale<FMT>(__uint_as_float(block_max[buf][slot]));
     // the maxima of the block before this one: every thread has read them, and
     // they are used again only after the next barrier
     if (tid < RP) block_max[buf == 0 ? 2 : buf - 1][tid] = 0;
     buf = buf == 2 ? 0 : buf + 1;
-    if (b < p.col_blocks && rr == 0 && col8 == 0) p.scales[rb * p.col_blocks + b] = s;
+    if (b < p.col_blocks && rr == 0 && col8 == 0) p.scales[rb * p.col_blocks + b] = s.s;
 #pragma unroll 1
     for (int j0 = 0; j0 < NP; j0 += U) {
       if constexpr (!kHeld) load(j0);
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const __grid_co
         const int r = rr + (j0 + j) * rp;
         float2 v[4];
         value(j0, j, v);
-        if (in && r < rows) store_codes<FMT>(p.q, (r0 + r) * p.cols + c, v, s, rcp);
+        if (in && r < rows) store_codes<FMT>(p.q + (r0 + r) * p.cols + c, v, s);
       }
     }
   }

@@ -107,12 +107,35 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 template <int FMT>
 constexpr float kFmax = FMT == BSGEMM_FP8_E5M2 ? 57344.0f : 448.0f;
 
-// A block's scale: amax / FMAX, or 1 where that is 0 (an empty block, or one
-// whose amax / FMAX is below the smallest FP32 value).
+// A block's scale and its reciprocal, each thread for itself.
+//   s = RN(amax / FMAX), or 1 where that is 0 (an empty block, or one whose
+//       amax / FMAX is below the smallest FP32 value);
+//   rcp = 1 / s to within FP32's last place, or 0 where amax lies outside the
+//       range that makes both quotients safe (the codes then take divisions).
+// The quotient by the constant is the product with its rounded reciprocal and
+// one correction by the exact remainder (Markstein): correctly rounded where
+// neither the quotient nor the remainder is near FP32's smallest values, which
+// the threshold keeps away; below it the division itself.
+constexpr float kSmallAmax = 0x1p-80f;
+
+struct Scale {
+  float s, rcp;
+};
+
 template <int FMT>
-__device__ __forceinline__ float block_scale(float amax) {
-  const float s = __fdiv_rn(amax, kFmax<FMT>);
-  return s > 0.f ? s : 1.f;
+__device__ __forceinline__ Scale block_scale(float amax) {
+  constexpr float inv = 1.0f / kFmax<FMT>;
+  Scale r;
+  if (amax >= kSmallAmax && amax < 0x1p127f) {
+    const float q = amax * inv;
+    r.s = __fmaf_rn(__fmaf_rn(-q, kFmax<FMT>, amax), inv, q);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.rcp) : "f"(r.s));
+  } else {
+    const float q = __fdiv_rn(amax, kFmax<FMT>);
+    r.s = q > 0.f ? q : 1.f;
+    r.rcp = q > 0.f ? 0.f : 1.f;
+  }
+  return r;
 }
 
 // FP8 codes of a (low byte) and b: round to nearest even, saturating.
@@ -122,23 +145,20 @@ __device__ __forceinline__ uint32_t encode2(float2 v) {
       __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, FMT == BSGEMM_FP8_E5M2 ? __NV_E5M2 : __NV_E4M3));
 }
 
-// Stores the codes of v / s. The quotient is v times the rounded reciprocal of
-// s: within 1.5 units of FP32's last place of the divided value, which is
-// itself that far from the exact one, against a code's half step of 2^-4. A
-// scale whose reciprocal could overflow takes the division.
-constexpr float kRcpMinScale = 0x1p-100f;
-
+// Stores the codes of v / s. The quotient is v times the reciprocal of s:
+// within 2 units of FP32's last place of the divided value, which is itself
+// that far from the exact one, against a code's half step of 2^-4.
 template <int FMT>
-__device__ __forceinline__ void store_codes(uint8_t* q, int64_t elem, const float2 (&v)[4], float s, float rs) {
+__device__ __forceinline__ void store_codes(uint8_t* q, const float2 (&v)[4], const Scale& s) {
   uint32_t c[4];
-  if (s >= kRcpMinScale) {
+  if (s.rcp > 0.f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = encode2<FMT>(mul2(v[i], both(rs)));
+    for (int i = 0; i < 4; ++i) c[i] = encode2<FMT>(mul2(v[i], both(s.rcp)));
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = encode2<FMT>(make_float2(__fdiv_rn(v[i].x, s), __fdiv_rn(v[i].y, s)));
+    for (int i = 0; i < 4; ++i) c[i] = encode2<FMT>(make_float2(__fdiv_rn(v[i].x, s.s), __fdiv_rn(v[i].y, s.s)));
   }
-  *reinterpret_cast<uint2*>(q + elem) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  *reinterpret_cast<uint2*>(q) = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 // Larger of a and the run's magnitudes; NaNs are passed over.

@@ -135,12 +135,10 @@ def rstd_rel(cols, g):
 
 
 def gelu_abs(z):
-    """FP32 bound of z Phi(z) beside its relative roundings: the fitted distribution function's 3e-7
-    (tests/test_sublayer_host.py has its parts) of |z|."""
-    return 3e-7 * z.abs().double()
+    """FP32 bound of z Phi(z) beside its own rounding: the fitted tail's (tests/test_sublayer_host.py has its parts)."""
+    return (1.1e-7 + 4 * U) * z.abs().double()
 
 
 def gelu_slope_abs(z):
-    """The same for Phi(z) + z phi(z): 3e-7 of the first; the density's exponent, -z^2/2 log2(e), is rounded twice
-    and the exponential and its factor three times more: |z| phi(z) (z^2 + 3) U, which is below 2 U."""
-    return torch.full_like(z, 3e-7 + 2 * U, dtype=torch.float64)
+    """The same for Phi(z) + z phi(z)."""
+    return torch.full_like(z, 1.1e-7 + 9 * U, dtype=torch.float64)

@@ -178,22 +178,30 @@ def test_plain_gradients_against_differences():
         assert (num - su.act_slope(z, name)).abs().max() < 1e-8
 
 
-def test_fitted_normal_distribution_function():
+def test_fitted_gelu():
     """The polynomial that the activation kernels evaluate, in FP32 steps, against 64 bits.
 
-    The lower tail exp(-u^2/2) Q(t) is 1/2 at most. Its relative error: 9e-8 of the fit, 2 roundings in t taken
-    twice (Q grows no faster than t^2 where the tail is large), 3 in the last steps of the polynomial, 1 in the
-    product: 9e-8 + 8 U = 5.7e-7, so 3e-7 in all; where the exponential's argument adds more, the tail is smaller.
+    T = Phi(-u) = 2^P <= 1/2 is off by 1.1e-7 of the fit and by ln 2 T times P's error in FP32, whose terms add up
+    to less than 2 |P| + 2 (two roundings of each, 4 U (|P| + 1)): ln 2 T 4 U (|P| + 1) <= 3 U, P being -1 at T = 1/2;
+    one more for the exponential. GELU: that times |z|, 1.1e-7 + 4 U = 3.5e-7, and its own rounding. The slope adds
+    u phi(u) <= 0.25 with (u^2 / 2 + 4) U of itself, below U, and three sums below 1.2: 5 U more, 6.5e-7.
     """
     src = open(os.path.join(ROOT, "fp8_block_scaled_bsgemm_b200", "csrc", "bsgemm_act.cu")).read()
-    p = float(re.search(r"kP = ([\d.]+)f", src).group(1))
-    coef = [float(c) for c in re.findall(r"q(?: = bsg::ffma2\(q, t,| =) both\((-?[\d.]+)f\)", src)]
-    assert len(coef) == 9
-    z = torch.linspace(0, 40, 400001, dtype=torch.float64).float()
-    t = 1 / (1 + torch.tensor(p) * z)
-    q = torch.full_like(t, coef[0])
-    for c in coef[1:]:
-        q = (q.double() * t.double() + torch.tensor(c).float().double()).float()
-    q = q * t
-    tail = torch.exp2(z * z * torch.tensor(-0.72134752)) * q
-    assert (tail.double() - su.phi(-z.double())).abs().max() < 3e-7
+    num = r"-?[\d.]+(?:e-\d+)?"
+    first = float(re.search(rf"t\[i\] = both\(({num})f\)", src).group(1))
+    coef = [float(c.strip().rstrip("f")) for c in re.search(r"coef\[6\] = \{([^}]*)\}", src).group(1).split(",")]
+    assert len(coef) == 6
+    z = torch.linspace(-20, 20, 800001, dtype=torch.float64).float()
+    n = -z.abs().clamp(max=14.0)
+    q = torch.full_like(z, first)
+    for c in coef:
+        q = (q.double() * n.double() + torch.tensor(c).double()).float()
+    t = torch.exp2(q)
+    gelu = (z.clamp(min=0).double() + t.double() * n.double()).float()
+    assert ((gelu.double() - su.act(z, "gelu")).abs() <= (1.1e-7 + 4 * su.U) * z.abs().double() + su.U * gelu.abs().double()).all()
+    phi = torch.exp2(((n * n).double() * -0.72134752 - 1.32574807).float())
+    h = (n.double() * phi.double() + (t - 0.5).double()).float()
+    slope = torch.where(z < 0, h, -h) + 0.5
+    assert (slope.double() - su.act_slope(z, "gelu")).abs().max() < 1.1e-7 + 9 * su.U
+    # past the clamp nothing is left of the tail
+    assert float(t[0]) < 2.0 ** -126
