@@ -403,12 +403,12 @@ def rms_norm_quantize(x, weight, residual=None, eps=1e-6, gran=128, fmt="e4m3", 
         if residual is not None:
             residual_out = torch.empty_like(x) if residual_out is None else \
                 _matrix(residual_out, "residual_out", x.dtype, dev, x.shape)
-        rstd = torch.empty((rows,), dtype=torch.float32, device=dev) if return_rstd else None
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
         st = lib().bsgemm_rms_norm_quantize_fp8(
             _SRC_DTYPES[x.dtype], _SRC_DTYPES[weight.dtype], FORMATS[fmt], x.data_ptr(),
             None if residual is None else residual.data_ptr(), weight.data_ptr(), float(eps), rows, cols, int(gran),
             None if residual is None else residual_out.data_ptr(), q.data_ptr(), scales.data_ptr(),
-            None if rstd is None else rstd.data_ptr(), _raw_stream(dev.index))
+            rstd.data_ptr(), _raw_stream(dev.index))
     if st != 0:
         raise BsgemmError(st, f"bsgemm_rms_norm_quantize_fp8 {rows}x{cols} g={gran}")
     h = x if residual is None else residual_out

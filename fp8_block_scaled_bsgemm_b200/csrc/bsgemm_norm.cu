@@ -17,9 +17,9 @@
 // All of it is memory-bound: 2-byte streams of 3 reads or writes per element
 // and a byte of codes forward, 4 backward.
 #include <cmath>
+#include <type_traits>
 
-#include "bsgemm_host.h"
-#include "bsgemm_rows.cuh"
+#include "bsgemm_blocks.cuh"
 
 namespace bsgn {
 
@@ -27,24 +27,23 @@ using namespace bsgr;
 
 // ------------------------------------------------------------------ forward
 //
-// A cluster of C CTAs takes one row of scale blocks (g rows, all columns);
-// CTA `rank` takes its blocks rank, rank + C, ... A row's mean square needs
-// every CTA's share, so each CTA writes the g partial sums it has into every
-// CTA of the cluster (distributed shared memory) and one cluster barrier
-// separates two passes over the CTA's blocks:
-//   pass 1: h = x + residual, stored, and its squares summed per row;
-//   pass 2: h is read again (by the thread that wrote it, from L2), scaled,
-//           and the block quantised.
-// Splitting the rows by columns this way keeps a block's amax inside one CTA,
-// and the only exchange is g floats per CTA. Sums are added in rank order, so
-// results do not vary between runs.
+// A row's mean square needs all its columns, a block's amax g rows: the two
+// cuts cross, so the work is done in two steps.
 //
-// A pass over a block takes rp rows at a time, g / 8 threads to a row. With
-// fewer rows than the 256 threads could take (a decode step), rp is cut to
-// them and the threads left over take other blocks at the same time.
-
-constexpr int kThreads = 256;
-constexpr int kMaxCluster = 16;
+// Many rows: two kernels. The first streams the rows (h = x + residual, its
+// squares summed, rstd written) at the memory's rate: 30 us of the 53 us that
+// 8192 x 4096 BF16 with residual takes. The second reads h again, partly from
+// L2 (x and residual are read as first to leave it), and is the block kernel of
+// bsgemm_blocks.cuh with y = h * rstd * weight for a value. Slabs of rows whose
+// h stays in L2 whole cost more in extra launches than they save (32 MB slabs:
+// 58 us). One kernel that holds a row of blocks across a cluster of up to 16
+// CTAs, exchanging row sums through distributed shared memory between two
+// passes, took 57 us there and 14.7 against 5.6 us on 128 x 7168: its passes
+// leave the memory idle at each barrier.
+//
+// Few rows (a decode step), where launches count: that one kernel, cut down to
+// rows that a CTA's threads take at once, with the values held in registers
+// between the passes.
 
 struct NormParams {
   const void* x;
@@ -55,196 +54,311 @@ struct NormParams {
   float* scales;
   float* rstd;
   int64_t rows, cols;
-  int col_blocks;
-  int cluster;
-  int row_log;      // log2 of the rows per pass
   int weight_bf16;
   float eps;
+  // few rows only
+  int col_blocks;
+  int cluster;
+  int row_log;      // log2 of the rows a CTA's threads take at once (all of them)
+  // many rows only
+  int tc_log;       // log2 of the threads to a row
 };
 
-__device__ __forceinline__ void load_weight(const NormParams& p, int64_t c, float2 (&w)[4]) {
-  if (p.weight_bf16) widen<true>(load_run<true>(p.weight, c), w);
-  else               widen<false>(load_run<false>(p.weight, c), w);
+__device__ __forceinline__ void load_weight(const void* weight, int is_bf16, int64_t c, float2 (&w)[4]) {
+  // (an input only, read for every row: kept in L1)
+  if (is_bf16) {
+    Run<true> r;
+    r.w[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(weight) + c));
+    widen<true>(r, w);
+  } else {
+    Run<false> r;
+    r.w[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(weight) + c));
+    r.w[1] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(weight) + c) + 1);
+    widen<false>(r, w);
+  }
 }
 
+// h = x + residual of a run, rounded to the type. (BF16: the packed addition
+// rounds the exact sum once; rounding to FP32 between changes nothing, since a
+// sum that needs more than FP32's 24 bits is far from BF16's borders.) It is
+// the rounded stream that is normalised: the next layer and the backward pass
+// read the same values.
+template <bool BF16>
+__device__ __forceinline__ Run<BF16> add_runs(const Run<BF16>& x, const Run<BF16>& r) {
+  Run<BF16> h;
+  if constexpr (BF16) {
+    const uint32_t a[4] = {x.w[0].x, x.w[0].y, x.w[0].z, x.w[0].w}, b[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(a[i]), "r"(b[i]));
+    h.w[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+    float2 v[4], u[4];
+    widen<BF16>(x, v);
+    widen<BF16>(r, u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = add2(v[i], u[i]);
+    h = narrow<BF16>(v);
+  }
+  return h;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 add_squares(const Run<BF16>& h, float2 s) {
+  float2 v[4];
+  widen<BF16>(h, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = bsg::ffma2(v[i], v[i], s);
+  return s;
+}
+
+__device__ __forceinline__ float rstd_of(const NormParams& p, float sum) {
+  return __frsqrt_rn(sum / static_cast<float>(p.cols) + p.eps);
+}
+
+// Rows, 2^tc_log threads to each (32 at least): a thread walks its columns,
+// four runs in flight.
+constexpr int kRowThreads = 256;
+
+template <bool BF16, bool RES>
+__global__ void __launch_bounds__(kRowThreads) norm_rows_kernel(const __grid_constant__ NormParams p) {
+  constexpr int U = BF16 ? 4 : 2;
+  __shared__ float warp_sum[kRowThreads / 32];
+  const int tid = threadIdx.x;
+  const int tc = 1 << p.tc_log;
+  const int t = tid & (tc - 1);
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (kRowThreads >> p.tc_log) + (tid >> p.tc_log);
+  bsg::grid_launch_dependents();
+  bsg::grid_dependency_wait();
+  const bool exists = r < p.rows;
+  float2 s = both(0.f);
+  if (exists) {
+    const int64_t base = r * p.cols;
+    const int cols = static_cast<int>(p.cols), stride = tc * kVec;
+    int c = t * kVec;
+    for (; c + (U - 1) * stride < cols; c += U * stride) {
+      Run<BF16> h[U], res[RES ? U : 1];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        h[j] = RES ? load_run_once<BF16>(p.x, base + c + j * stride) : load_run<BF16>(p.x, base + c + j * stride);
+        if constexpr (RES) res[j] = load_run_once<BF16>(p.residual, base + c + j * stride);
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if constexpr (RES) {
+          h[j] = add_runs<BF16>(h[j], res[j]);
+          store_run<BF16>(p.stream_out, base + c + j * stride, h[j]);
+        }
+        s = add_squares<BF16>(h[j], s);
+      }
+    }
+    for (; c < cols; c += stride) {
+      Run<BF16> h = RES ? load_run_once<BF16>(p.x, base + c) : load_run<BF16>(p.x, base + c);
+      if constexpr (RES) {
+        h = add_runs<BF16>(h, load_run_once<BF16>(p.residual, base + c));
+        store_run<BF16>(p.stream_out, base + c, h);
+      }
+      s = add_squares<BF16>(h, s);
+    }
+  }
+  float sum = s.x + s.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (tc > 32) {
+    if ((tid & 31) == 0) warp_sum[tid / 32] = sum;
+    __syncthreads();
+    sum = 0.f;
+    for (int k = 0; k < tc / 32; ++k) sum += warp_sum[((tid >> p.tc_log) << (p.tc_log - 5)) + k];
+  }
+  if (exists && t == 0) p.rstd[r] = rstd_of(p, sum);
+}
+
+// The block kernel's values: h * rstd * weight.
+struct Scaled {
+  const float* rstd;
+  const void* weight;
+  int weight_bf16;
+  static constexpr int kInputs = 1;
+  static constexpr bool kSums = false;
+  template <int NP>
+  struct Rows {
+    float rs[NP];
+  };
+  struct Cols {
+    float2 w[4];
+  };
+  template <int NP>
+  __device__ __forceinline__ Rows<NP> rows(int64_t row, int left, int step) const {
+    Rows<NP> r;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) r.rs[j] = j * step < left ? __ldg(rstd + row + j * step) : 0.f;
+    return r;
+  }
+  __device__ __forceinline__ Cols cols(int col, bool exists) const {
+    Cols c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.w[i] = both(0.f);
+    if (exists) load_weight(weight, weight_bf16, col, c.w);
+    return c;
+  }
+  template <int NP>
+  __device__ __forceinline__ void apply(const Rows<NP>& r, const Cols& c, int j, float2 (&v)[4],
+                                        const float2 (&)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(v[i], both(r.rs[j])), c.w[i]);
+  }
+};
+
+// Few rows: at most kFewThreads / (g / 8), all in one row of blocks. A cluster
+// of C CTAs takes it, 2^row_log rows at once and the threads left over other
+// blocks at the same time (`slots` of them): CTA `rank` takes blocks rank + C *
+// slot, and so on by C * slots. kFewKeep blocks of a thread stay in registers
+// between the passes; where there are more they are read again.
+constexpr int kFewThreads = 256;
+constexpr int kFewKeep = 4;
+constexpr int kMaxCluster = 16;
+template <int G>
+constexpr int kFewRows = kFewThreads / (G / kVec);
+
 template <int G, bool BF16, int FMT, bool RES>
-__global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kFewThreads) norm_few_kernel(const __grid_constant__ NormParams p) {
   constexpr int L = G / kVec;          // threads to a row of a block
-  constexpr int RP = kThreads / L;     // rows the CTA takes at a time (rp at most)
-  constexpr int NP = G / RP;           // passes over a full block
-  // passes loaded at a time, so that many loads are in flight at once; where
-  // they cover the block its values also stay in registers for the encoding
-  constexpr int U = NP < (BF16 ? 8 : 4) ? NP : (BF16 ? 8 : 4);
-  constexpr bool kHeld = U == NP;
-  __shared__ float part[kMaxCluster][G];  // the row sums of each CTA of the cluster
-  __shared__ float own_sum[G];
-  __shared__ float row_rstd[G];
-  __shared__ uint32_t block_max[3][kThreads / L];
+  constexpr int RP = kFewRows<G>;
+  constexpr int K = kFewKeep;
+  __shared__ float part[kMaxCluster][RP];  // the row sums of each CTA of the cluster
+  __shared__ float own_sum[RP];
+  __shared__ float row_rstd[RP];
+  __shared__ uint32_t block_max[3][K][RP];
 
   const int tid = threadIdx.x;
   const int rank = p.cluster > 1 ? static_cast<int>(bsg::cluster_ctarank()) : 0;
-  const int64_t rb = blockIdx.x / p.cluster;
-  const int64_t r0 = rb * G;
-  const int rows = static_cast<int>(p.rows - r0 < G ? p.rows - r0 : G);
+  const int rows = static_cast<int>(p.rows);
   const int rp = 1 << p.row_log;
-  const int slots = RP >> p.row_log;   // blocks taken at the same time
+  const int slots = RP >> p.row_log;
   const int col8 = (tid % L) * kVec;
   const int rr = (tid / L) & (rp - 1);
   const int slot = (tid / L) >> p.row_log;
-  const int step = p.cluster * slots;  // col_blocks + step stays far below 2^31
+  const int step = p.cluster * slots;      // col_blocks + K * step stays far below 2^31
+  const int64_t base = rr * p.cols + col8;
 
-  if (tid < 3 * RP) (&block_max[0][0])[tid] = 0;
+  for (int i = tid; i < 3 * K * RP; i += kFewThreads) (&block_max[0][0][0])[i] = 0;
   bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
 
-  // ---- pass 1
-  float ss[NP];
+  auto inside = [&](int b) {
+    return rr < rows && b < p.col_blocks && static_cast<int64_t>(b) * G + col8 < p.cols;
+  };
+  // ---- pass 1: h and its squares
+  Run<BF16> h[K], keep[K];
+  float2 ss = both(0.f);
+  for (int b0 = rank + p.cluster * slot; b0 < p.col_blocks; b0 += K * step) {
+    Run<BF16> res[RES ? K : 1];
 #pragma unroll
-  for (int j = 0; j < NP; ++j) ss[j] = 0.f;
-  for (int b = rank + p.cluster * slot; b < p.col_blocks; b += step) {
-    const int64_t c = static_cast<int64_t>(b) * G + col8;
-    if (c >= p.cols) continue;
-#pragma unroll
-    for (int j0 = 0; j0 < NP; j0 += U) {
-      Run<BF16> xr[U], res[RES ? U : 1];
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int r = rr + (j0 + j) * rp;
-        xr[j] = zero_run<BF16>();
-        if constexpr (RES) res[j] = zero_run<BF16>();
-        if (r < rows) {
-          xr[j] = load_run<BF16>(p.x, (r0 + r) * p.cols + c);
-          if constexpr (RES) res[j] = load_run<BF16>(p.residual, (r0 + r) * p.cols + c);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int r = rr + (j0 + j) * rp;
-        float2 v[4];
-        widen<BF16>(xr[j], v);
-        if constexpr (RES) {
-          float2 u[4];
-          widen<BF16>(res[j], u);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = add2(v[i], u[i]);
-          // the stream is rounded to its type here, once, and it is the
-          // rounded stream that is normalised: the next layer and the
-          // backward pass read the same values
-          const Run<BF16> h = narrow<BF16>(v);
-          if (r < rows) store_run<BF16>(p.stream_out, (r0 + r) * p.cols + c, h);
-          widen<BF16>(h, v);
-        }
-        float2 s = mul2(v[0], v[0]);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) s = bsg::ffma2(v[i], v[i], s);
-        ss[j0 + j] += s.x + s.y;
+    for (int k = 0; k < K; ++k) {
+      const int b = b0 + k * step;
+      h[k] = zero_run<BF16>();
+      if constexpr (RES) res[k] = zero_run<BF16>();
+      if (inside(b)) {
+        h[k] = load_run<BF16>(p.x, base + static_cast<int64_t>(b) * G);
+        if constexpr (RES) res[k] = load_run<BF16>(p.residual, base + static_cast<int64_t>(b) * G);
       }
     }
-  }
 #pragma unroll
-  for (int j = 0; j < NP; ++j) {
+    for (int k = 0; k < K; ++k) {
+      if constexpr (RES) {
+        const int b = b0 + k * step;
+        h[k] = add_runs<BF16>(h[k], res[k]);
+        if (inside(b)) store_run<BF16>(p.stream_out, base + static_cast<int64_t>(b) * G, h[k]);
+      }
+      ss = add_squares<BF16>(h[k], ss);
+    }
+    if (b0 == rank + p.cluster * slot) {
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
-    // row rr + j * rp of slot 0..slots-1; where rp < RP only j = 0 has rows
-    if (tid % L == 0 && (rp == RP || j == 0)) own_sum[j * RP + tid / L] = ss[j];
+      for (int k = 0; k < K; ++k) keep[k] = h[k];
+    }
   }
+  float sum = ss.x + ss.y;
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (tid % L == 0) own_sum[tid / L] = sum;
   __syncthreads();
-  for (int r = tid; r < rows; r += kThreads) {
-    float s = own_sum[r];
-    for (int k = 1; k < slots; ++k) s += own_sum[k * rp + r];
+  if (tid < rows) {
+    float s = own_sum[tid];
+    for (int k = 1; k < slots; ++k) s += own_sum[k * rp + tid];
     if (p.cluster == 1) {
-      part[0][r] = s;
+      part[0][tid] = s;
     } else {
-      const uint32_t mine = bsg::smem_addr(&part[rank][r]);
+      const uint32_t mine = bsg::smem_addr(&part[rank][tid]);
       for (int d = 0; d < p.cluster; ++d) st_cluster_f32(bsg::mapa_shared(mine, d), s);
     }
   }
-  // every thread of the cluster arrives, also in CTAs without blocks; after it
-  // no CTA touches another's shared memory, so any may run on to its exit
+  // every thread of the cluster arrives; after it no CTA touches another's
+  // shared memory, so any may run on to its exit
   __syncwarp();
   if (p.cluster > 1) bsg::cluster_sync_all();
   else __syncthreads();
-  for (int r = tid; r < rows; r += kThreads) {
-    float s = part[0][r];
-    for (int k = 1; k < p.cluster; ++k) s += part[k][r];
-    const float v = __frsqrt_rn(s / static_cast<float>(p.cols) + p.eps);
-    row_rstd[r] = v;
-    if (rank == 0 && p.rstd != nullptr) p.rstd[r0 + r] = v;
+  if (tid < rows) {
+    float s = part[0][tid];
+    for (int k = 1; k < p.cluster; ++k) s += part[k][tid];
+    const float v = rstd_of(p, s);
+    row_rstd[tid] = v;
+    if (rank == 0) p.rstd[tid] = v;
   }
   __syncthreads();
 
-  // ---- pass 2
+  // ---- pass 2: K blocks of each slot at a time, with one barrier
+  const float rs = rr < rows ? row_rstd[rr] : 0.f;
   const void* h_src = RES ? p.stream_out : p.x;
   int buf = 0;
-  for (int base = rank; base < p.col_blocks; base += step) {
-    const int b = base + p.cluster * slot;
-    const int64_t c = static_cast<int64_t>(b) * G + col8;
-    const bool in = b < p.col_blocks && c < p.cols;
-    float2 w[4];
+  for (int first = rank; first < p.col_blocks; first += K * step) {
+    const int b0 = first + p.cluster * slot;
+    float2 v[K][4];
+    if (first == rank) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = both(0.f);
-    if (in) load_weight(p, c, w);
-    Run<BF16> h[U];
-    auto load = [&](int j0) {
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int r = rr + (j0 + j) * rp;
-        h[j] = zero_run<BF16>();
-        if (in && r < rows) h[j] = load_run<BF16>(h_src, (r0 + r) * p.cols + c);
-      }
-    };
-    // y of the loaded row j0 + j
-    auto value = [&](int j0, int j, float2 (&v)[4]) {
-      const int r = rr + (j0 + j) * rp;
-      const float rs = r < rows ? row_rstd[r] : 0.f;
-      widen<BF16>(h[j], v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(v[i], both(rs)), w[i]);
-    };
-    float amax = 0.f;
-#pragma unroll 1
-    for (int j0 = 0; j0 < NP; j0 += U) {
-      load(j0);
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        float2 v[4];
-        value(j0, j, v);
-        amax = max_abs(amax, v);
-      }
-    }
-    // magnitudes are not negative, so their bit patterns order as they do
-    if (slots == 1) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-      if ((tid & 31) == 0) atomicMax(&block_max[buf][0], m);
+      for (int k = 0; k < K; ++k) h[k] = keep[k];
     } else {
 #pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (tid % L == 0) atomicMax(&block_max[buf][slot], __float_as_uint(amax));
-    }
-    __syncthreads();
-    const Scale s = block_scale<FMT>(__uint_as_float(block_max[buf][slot]));
-    // the maxima of the block before this one: every thread has read them, and
-    // they are used again only after the next barrier
-    if (tid < RP) block_max[buf == 0 ? 2 : buf - 1][tid] = 0;
-    buf = buf == 2 ? 0 : buf + 1;
-    if (b < p.col_blocks && rr == 0 && col8 == 0) p.scales[rb * p.col_blocks + b] = s.s;
-#pragma unroll 1
-    for (int j0 = 0; j0 < NP; j0 += U) {
-      if constexpr (!kHeld) load(j0);
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int r = rr + (j0 + j) * rp;
-        float2 v[4];
-        value(j0, j, v);
-        if (in && r < rows) store_codes<FMT>(p.q + (r0 + r) * p.cols + c, v, s);
+      for (int k = 0; k < K; ++k) {
+        h[k] = zero_run<BF16>();
+        if (inside(b0 + k * step)) h[k] = load_run<BF16>(h_src, base + static_cast<int64_t>(b0 + k * step) * G);
       }
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int b = b0 + k * step;
+      float2 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = both(0.f);
+      if (inside(b)) load_weight(p.weight, p.weight_bf16, static_cast<int64_t>(b) * G + col8, w);
+      widen<BF16>(h[k], v[k]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[k][i] = mul2(mul2(v[k][i], both(rs)), w[i]);
+      // magnitudes are not negative, so their bit patterns order as they do
+      float amax = max_abs(0.f, v[k]);
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (tid % L == 0) atomicMax(&block_max[buf][k][slot], __float_as_uint(amax));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int b = b0 + k * step;
+      if (b < p.col_blocks) {
+        const Scale s = block_scale<FMT>(__uint_as_float(block_max[buf][k][slot]));
+        if (rr == 0 && col8 == 0) p.scales[b] = s.s;
+        if (inside(b)) store_codes<FMT>(p.q + base + static_cast<int64_t>(b) * G, v[k], s);
+      }
+    }
+    // the maxima of the round before this one: every thread has read them, and
+    // they are used again only after the next barrier
+    for (int i = tid; i < K * RP; i += kFewThreads) (&block_max[buf == 0 ? 2 : buf - 1][0][0])[i] = 0;
+    buf = buf == 2 ? 0 : buf + 1;
   }
 }
 
 template <int G, bool BF16, int FMT, bool RES>
-bsgemm_status launch_norm(NormParams& p, cudaStream_t stream, const bsg_host::DeviceInfo& dev) {
-  auto kern = norm_quant_kernel<G, BF16, FMT, RES>;
+bsgemm_status launch_few(NormParams& p, cudaStream_t stream, const bsg_host::DeviceInfo& dev) {
+  auto kern = norm_few_kernel<G, BF16, FMT, RES>;
   static bsg_host::PerDeviceOnce setup;
   if (!setup.done(dev.ordinal)) {
     // clusters of 16 are beyond the portable size
@@ -252,43 +366,67 @@ bsgemm_status launch_norm(NormParams& p, cudaStream_t stream, const bsg_host::De
       return BSGEMM_ERR_CUDA;
     setup.mark(dev.ordinal);
   }
-  constexpr int RP = kThreads / (G / kVec);
+  p.col_blocks = static_cast<int>((p.cols + G - 1) / G);
   p.row_log = 0;
-  while ((1 << p.row_log) < RP && (int64_t{1} << p.row_log) < p.rows) ++p.row_log;
+  while ((1 << p.row_log) < p.rows) ++p.row_log;
+  // as many CTAs as have blocks for all their slots, at most 16
   p.cluster = 1;
-  while (p.cluster < kMaxCluster && 2 * p.cluster <= p.col_blocks) p.cluster *= 2;
-  const int64_t row_blocks = (p.rows + G - 1) / G;
-  return launch_rows(kern, row_blocks * p.cluster, kThreads, 0, p.cluster, stream, p);
+  while (p.cluster < kMaxCluster && p.cluster * (kFewRows<G> >> p.row_log) < p.col_blocks) p.cluster *= 2;
+  return launch_rows(kern, p.cluster, kFewThreads, 0, p.cluster, stream, p);
 }
 
-template <int G>
-bsgemm_status norm_of(int src, int fmt, NormParams& p, cudaStream_t st, const bsg_host::DeviceInfo& dev) {
-  p.col_blocks = static_cast<int>((p.cols + G - 1) / G);
-  const bool bf16 = src == BSGEMM_SRC_BF16, e5 = fmt == BSGEMM_FP8_E5M2, res = p.residual != nullptr;
-#define BSGN_GO(B, F) \
-  return res ? launch_norm<G, B, F, true>(p, st, dev) : launch_norm<G, B, F, false>(p, st, dev)
-  if (bf16 && !e5) BSGN_GO(true, BSGEMM_FP8_E4M3);
-  if (bf16) BSGN_GO(true, BSGEMM_FP8_E5M2);
-  if (!e5) BSGN_GO(false, BSGEMM_FP8_E4M3);
-  BSGN_GO(false, BSGEMM_FP8_E5M2);
-#undef BSGN_GO
+template <int G, bool BF16, int FMT>
+bsgemm_status few_of(NormParams& p, cudaStream_t st, const bsg_host::DeviceInfo& dev) {
+  return p.residual ? launch_few<G, BF16, FMT, true>(p, st, dev) : launch_few<G, BF16, FMT, false>(p, st, dev);
+}
+
+template <int G, bool BF16>
+bsgemm_status few_of(int fmt, NormParams& p, cudaStream_t st, const bsg_host::DeviceInfo& dev) {
+  return fmt == BSGEMM_FP8_E5M2 ? few_of<G, BF16, BSGEMM_FP8_E5M2>(p, st, dev)
+                                : few_of<G, BF16, BSGEMM_FP8_E4M3>(p, st, dev);
+}
+
+template <bool BF16>
+bsgemm_status norm_of(int fmt, int gran, NormParams& p, cudaStream_t st, const bsg_host::DeviceInfo& dev) {
+  if (gran == 64 && p.rows <= kFewRows<64>) return few_of<64, BF16>(fmt, p, st, dev);
+  if (gran == 128 && p.rows <= kFewRows<128>) return few_of<128, BF16>(fmt, p, st, dev);
+  if (gran == 256 && p.rows <= kFewRows<256>) return few_of<256, BF16>(fmt, p, st, dev);
+  // threads to a row: 32 where the rows fill the GPU with warps (1024 threads
+  // to an SM), else more, as far as there are runs for them
+  p.tc_log = 5;
+  while ((1 << p.tc_log) < kRowThreads && (kVec << p.tc_log) < p.cols &&
+         (p.rows << p.tc_log) < int64_t{dev.num_sms} * 1024)
+    ++p.tc_log;
+  const int64_t per_cta = kRowThreads >> p.tc_log;
+  auto kern = p.residual ? norm_rows_kernel<BF16, true> : norm_rows_kernel<BF16, false>;
+  bsgemm_status s = launch_rows(kern, (p.rows + per_cta - 1) / per_cta, kRowThreads, 0, 1, st, p);
+  if (s != BSGEMM_OK) return s;
+  BlockParams b{};
+  b.in0 = p.residual ? p.stream_out : p.x;
+  b.q = p.q;
+  b.scales = p.scales;
+  b.rows = p.rows;
+  b.cols = p.cols;
+  return launch_blocks<BF16>(gran, fmt, b, Scaled{p.rstd, p.weight, p.weight_bf16}, st, dev);
 }
 
 // ------------------------------------------------------------------ backward
 //
 // A row's gradient needs one sum over its columns (dy * weight * h), so a row
 // is read once into registers: a cluster of C CTAs takes the columns of a row
-// in slices of at most 4096, a run to a thread, and the CTA's 512 threads take
-// 512 / TC rows at a time where a slice needs only TC of them. Each thread
-// keeps the sums of dy * n of its 8 columns over all its rows; at the end they
+// in slices of at most 4096, two runs to a thread, and the CTA's 256 threads
+// take 256 / TC rows at a time where a slice needs only TC of them. Each thread
+// keeps the sums of dy * n of its 16 columns over all its rows; at the end they
 // are added over the CTA's row groups and written as one row of partial sums,
 // and a second kernel adds those rows in order (no atomics: the order never
 // changes).
 
-constexpr int kBwdThreads = 512;
-constexpr int kBwdRows = 2;          // rows a thread holds at a time
+constexpr int kBwdThreads = 256;
+constexpr int kBwdRuns = 2;          // runs to a thread, TC * 8 columns apart
 constexpr int kBwdMaxParts = 512;    // rows of partial sums at most
-constexpr int64_t kBwdMaxCols = int64_t{kMaxCluster} * kBwdThreads * kVec;
+constexpr int64_t kBwdMaxCols = int64_t{kMaxCluster} * kBwdThreads * kBwdRuns * kVec;
+template <bool BF16>
+constexpr int kBwdCtasPerSm = BF16 ? 3 : 2;
 
 struct NormBwdParams {
   const void* dy;
@@ -307,128 +445,131 @@ struct NormBwdParams {
 };
 
 template <bool BF16, bool SKIP>
-__global__ void __launch_bounds__(kBwdThreads, BF16 ? 2 : 1)
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtasPerSm<BF16>)
     norm_backward_kernel(const __grid_constant__ NormBwdParams p) {
-  constexpr int R = kBwdRows;
+  constexpr int V = kBwdRuns;
   constexpr int kWarps = kBwdThreads / 32;
-  __shared__ float warp_sum[2][R][kWarps];
-  __shared__ float cta_sum[2][R][kMaxCluster][kBwdThreads / 32];  // per row group (TC >= 32: at most 16)
-  __shared__ float2 dw_sum[kBwdThreads * 4];
+  __shared__ float warp_sum[2][kWarps];
+  __shared__ float cta_sum[2][kMaxCluster];   // a cluster's CTAs take one row at a time
+  __shared__ float2 dw_sum[V * 4][kBwdThreads];
 
-  const int tid = threadIdx.x, warp = tid / 32;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   const int rank = p.cluster > 1 ? static_cast<int>(bsg::cluster_ctarank()) : 0;
   const int part = blockIdx.x / p.cluster;
   const int tc = 1 << p.tc_log;
   const int groups = kBwdThreads >> p.tc_log;
   const int group = tid >> p.tc_log;
-  const int warps_per_group = tc / 32;
-  const int local = (tid & (tc - 1)) * kVec;
-  const int64_t c = static_cast<int64_t>(rank) * p.slice + local;
-  const bool in_cols = local < p.slice && c < p.cols;
+  const int group_warps = tc / 32;
+  const int run0 = (tid & (tc - 1)) * kVec;   // within the slice; run v is v * tc * 8 on
+  const int64_t c0 = static_cast<int64_t>(rank) * p.slice + run0;
+  bool in[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) in[v] = run0 + v * tc * kVec < p.slice && c0 + v * tc * kVec < p.cols;
 
   bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
 
-  float2 w[4], dw[4];
+  float2 w[V][4], dw[V][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = dw[i] = both(0.f);
-  if (in_cols) {
-    if (p.weight_bf16) widen<true>(load_run<true>(p.weight, c), w);
-    else               widen<false>(load_run<false>(p.weight, c), w);
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[v][i] = dw[v][i] = both(0.f);
+    if (in[v]) load_weight(p.weight, p.weight_bf16, c0 + v * tc * kVec, w[v]);
   }
   const float inv_cols = 1.0f / static_cast<float>(p.cols);
 
+  // the part's rows: `groups` at a time, dealt out in turn
+  const int64_t stride = static_cast<int64_t>(p.parts) * groups;
+  int64_t r = static_cast<int64_t>(part) * groups + group;
+  int64_t e = r * p.cols + c0;
+  const int64_t e_step = stride * p.cols;
   int buf = 0;
-  // the part's rows: batches of groups * R, dealt out in turn
-  const int64_t batch = static_cast<int64_t>(groups) * R;
-  for (int64_t base = part * batch; base < p.rows; base += p.parts * batch) {
-    Run<BF16> dy[R], h[R], sk[SKIP ? R : 1];
-    float rs[R], dot[R];
+  for (int64_t base = static_cast<int64_t>(part) * groups; base < p.rows; base += stride) {
+    const bool exists = r < p.rows;
+    Run<BF16> dy[V], h[V], sk[SKIP ? V : 1];
+    float rs = 0.f;
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int64_t r = base + j * groups + group;
-      dy[j] = h[j] = zero_run<BF16>();
-      if constexpr (SKIP) sk[j] = zero_run<BF16>();
-      rs[j] = 0.f;
-      if (in_cols && r < p.rows) {
-        dy[j] = load_run<BF16>(p.dy, r * p.cols + c);
-        h[j] = load_run<BF16>(p.h, r * p.cols + c);
-        if constexpr (SKIP) sk[j] = load_run<BF16>(p.skip, r * p.cols + c);
-        rs[j] = __ldg(p.rstd + r);
+    for (int v = 0; v < V; ++v) {
+      dy[v] = h[v] = zero_run<BF16>();
+      if constexpr (SKIP) sk[v] = zero_run<BF16>();
+      if (in[v] && exists) {
+        dy[v] = load_run<BF16>(p.dy, e + v * tc * kVec);
+        h[v] = load_run<BF16>(p.h, e + v * tc * kVec);
+        if constexpr (SKIP) sk[v] = load_run<BF16>(p.skip, e + v * tc * kVec);
       }
     }
+    if (exists) rs = __ldg(p.rstd + r);
+    float2 s2 = both(0.f);
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
+    for (int v = 0; v < V; ++v) {
       float2 a[4], b[4];
-      widen<BF16>(dy[j], a);
-      widen<BF16>(h[j], b);
-      float2 s = both(0.f);
+      widen<BF16>(dy[v], a);
+      widen<BF16>(h[v], b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 n = mul2(b[i], both(rs[j]));
-        dw[i] = bsg::ffma2(a[i], n, dw[i]);
-        s = bsg::ffma2(mul2(a[i], w[i]), n, s);
+        const float2 n = mul2(b[i], both(rs));
+        dw[v][i] = bsg::ffma2(a[i], n, dw[v][i]);
+        s2 = bsg::ffma2(mul2(a[i], w[v][i]), n, s2);
       }
-      dot[j] = s.x + s.y;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-      if ((tid & 31) == 0) warp_sum[buf][j][warp] = dot[j];
     }
-    __syncthreads();
-    if (p.cluster > 1) {
-      // (slices of a cluster have 4096 columns at most, half of that at
-      // least: tc is 256 or 512 and there are few groups)
-      if (tid < R * groups) {
-        const int j = tid / groups, g = tid % groups;
-        float s = 0.f;
-        for (int k = 0; k < warps_per_group; ++k) s += warp_sum[buf][j][g * warps_per_group + k];
-        const uint32_t mine = bsg::smem_addr(&cta_sum[buf][j][rank][g]);
-        for (int d = 0; d < p.cluster; ++d) st_cluster_f32(bsg::mapa_shared(mine, d), s);
-      }
-      __syncwarp();
-      bsg::cluster_sync_all();
-    }
+    float s = s2.x + s2.y;
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int64_t r = base + j * groups + group;
-      float s = 0.f;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (group_warps > 1 || p.cluster > 1) {
+      if (lane == 0) warp_sum[buf][warp] = s;
+      __syncthreads();
+      // the group's warps, a lane to each: the same order in all of them
+      s = warp_sum[buf][(warp & ~(group_warps - 1)) + (lane & (group_warps - 1))];
+      for (int o = group_warps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (p.cluster > 1) {
-        for (int k = 0; k < p.cluster; ++k) s += cta_sum[buf][j][k][group];
-      } else {
-        for (int k = 0; k < warps_per_group; ++k) s += warp_sum[buf][j][group * warps_per_group + k];
+        // (slices of a cluster have more than 2048 columns: one row group)
+        if (tid < p.cluster) st_cluster_f32(bsg::mapa_shared(bsg::smem_addr(&cta_sum[buf][rank]), tid), s);
+        __syncwarp();
+        bsg::cluster_sync_all();
+        s = cta_sum[buf][0];
+        for (int k = 1; k < p.cluster; ++k) s += cta_sum[buf][k];
       }
-      const float m = s * inv_cols;   // mean(dn * n)
+    }
+    const float m = s * inv_cols;   // mean(dn * n)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
       float2 a[4], b[4];
-      widen<BF16>(dy[j], a);
-      widen<BF16>(h[j], b);
+      widen<BF16>(dy[v], a);
+      widen<BF16>(h[v], b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 n = mul2(b[i], both(rs[j]));
-        const float2 dn = mul2(a[i], w[i]);
-        a[i] = mul2(bsg::ffma2(n, both(-m), dn), both(rs[j]));
+        const float2 n = mul2(b[i], both(rs));
+        a[i] = mul2(bsg::ffma2(n, both(-m), mul2(a[i], w[v][i])), both(rs));
       }
       if constexpr (SKIP) {
-        widen<BF16>(sk[j], b);
+        widen<BF16>(sk[v], b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = add2(a[i], b[i]);
       }
-      if (in_cols && r < p.rows) store_run<BF16>(p.dx, r * p.cols + c, narrow<BF16>(a));
+      if (in[v] && exists) store_run<BF16>(p.dx, e + v * tc * kVec, narrow<BF16>(a));
     }
-    // the sums are double-buffered: a thread writes a buffer again two batches
+    r += stride;
+    e += e_step;
+    // the sums are double-buffered: a thread writes a buffer again two rows
     // on, past a barrier that follows every read of it
     buf ^= 1;
   }
 
   // the row groups' sums, added in order by the first group's threads
-  const int t = tid & (tc - 1);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dw_sum[i * kBwdThreads + tid] = dw[i];
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw_sum[v * 4 + i][tid] = dw[v][i];
   __syncthreads();
-  if (group == 0 && in_cols) {
-    for (int g = 1; g < groups; ++g)
+  if (group == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dw[i] = add2(dw[i], dw_sum[i * kBwdThreads + (g << p.tc_log) + t]);
-    store_run<false>(p.part, static_cast<int64_t>(part) * p.cols + c, narrow<false>(dw));
+    for (int v = 0; v < V; ++v) {
+      for (int g = 1; g < groups; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw[v][i] = add2(dw[v][i], dw_sum[v * 4 + i][(g << p.tc_log) + tid]);
+      if (in[v])
+        store_run<false>(p.part, static_cast<int64_t>(part) * p.cols + c0 + v * tc * kVec, narrow<false>(dw[v]));
+    }
   }
 }
 
@@ -470,7 +611,7 @@ extern "C" bsgemm_status bsgemm_rms_norm_quantize_fp8(int src_dtype, int weight_
                                                       float eps, int64_t rows, int64_t cols, int gran,
                                                       void* residual_out, void* q, float* scales, float* rstd,
                                                       bsgemm_stream_t stream) {
-  if (!x || !weight || !q || !scales || (residual != nullptr) != (residual_out != nullptr))
+  if (!x || !weight || !q || !scales || !rstd || (residual != nullptr) != (residual_out != nullptr))
     return BSGEMM_ERR_INVALID_ARG;
   if (weight_dtype != BSGEMM_SRC_F32 && weight_dtype != BSGEMM_SRC_BF16) return BSGEMM_ERR_INVALID_ARG;
   if (fp8_format != BSGEMM_FP8_E4M3 && fp8_format != BSGEMM_FP8_E5M2) return BSGEMM_ERR_INVALID_ARG;
@@ -510,11 +651,8 @@ extern "C" bsgemm_status bsgemm_rms_norm_quantize_fp8(int src_dtype, int weight_
   p.weight_bf16 = weight_dtype == BSGEMM_SRC_BF16;
   p.eps = eps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  switch (gran) {
-    case 64:  return bsgn::norm_of<64>(src_dtype, fp8_format, p, s, dev);
-    case 128: return bsgn::norm_of<128>(src_dtype, fp8_format, p, s, dev);
-    default:  return bsgn::norm_of<256>(src_dtype, fp8_format, p, s, dev);
-  }
+  return src_dtype == BSGEMM_SRC_BF16 ? bsgn::norm_of<true>(fp8_format, gran, p, s, dev)
+                                      : bsgn::norm_of<false>(fp8_format, gran, p, s, dev);
 }
 
 extern "C" size_t bsgemm_rms_norm_backward_workspace(int64_t rows, int64_t cols) {
@@ -563,14 +701,14 @@ extern "C" bsgemm_status bsgemm_rms_norm_backward(int src_dtype, int weight_dtyp
   p.cols = cols;
   p.weight_bf16 = weight_dtype == BSGEMM_SRC_BF16;
   p.cluster = 1;
-  while (int64_t{p.cluster} * bsgn::kBwdThreads * bsgr::kVec < cols) p.cluster *= 2;
+  while (int64_t{p.cluster} * bsgn::kBwdThreads * bsgn::kBwdRuns * bsgr::kVec < cols) p.cluster *= 2;
   const int64_t runs = cols / bsgr::kVec;
   p.slice = static_cast<int>((runs + p.cluster - 1) / p.cluster * bsgr::kVec);
   p.tc_log = 5;
-  while ((bsgr::kVec << p.tc_log) < p.slice) ++p.tc_log;
-  const int64_t batch = int64_t{bsgn::kBwdThreads >> p.tc_log} * bsgn::kBwdRows;
+  while ((bsgn::kBwdRuns * bsgr::kVec << p.tc_log) < p.slice) ++p.tc_log;
+  const int64_t batch = bsgn::kBwdThreads >> p.tc_log;
   const int64_t batches = (rows + batch - 1) / batch;
-  int64_t parts = int64_t{dev.num_sms} * (bf16 ? 2 : 1) / p.cluster;
+  int64_t parts = int64_t{dev.num_sms} * (bf16 ? bsgn::kBwdCtasPerSm<true> : bsgn::kBwdCtasPerSm<false>) / p.cluster;
   if (parts < 1) parts = 1;
   if (parts > batches) parts = batches;
   if (parts > bsgn::kBwdMaxParts) parts = bsgn::kBwdMaxParts;

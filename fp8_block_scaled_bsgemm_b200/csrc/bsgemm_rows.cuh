@@ -8,7 +8,6 @@
 // multiples of 16 columns, so a run lies wholly inside the matrix or outside.
 #pragma once
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -44,6 +43,16 @@ __device__ __forceinline__ Run<BF16> load_run(const void* base, int64_t elem) {
   const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + elem * (BF16 ? 2 : 4));
 #pragma unroll
   for (int h = 0; h < (BF16 ? 1 : 2); ++h) r.w[h] = __ldcg(p + h);
+  return r;
+}
+
+// The same for data that is not read again soon: first to leave L2.
+template <bool BF16>
+__device__ __forceinline__ Run<BF16> load_run_once(const void* base, int64_t elem) {
+  Run<BF16> r;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + elem * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int h = 0; h < (BF16 ? 1 : 2); ++h) r.w[h] = __ldcs(p + h);
   return r;
 }
 
@@ -138,11 +147,31 @@ __device__ __forceinline__ Scale block_scale(float amax) {
   return r;
 }
 
-// FP8 codes of a (low byte) and b: round to nearest even, saturating.
+// FP8 codes of four values, the first in the lowest byte: round to nearest even,
+// saturating. (As one assembly block the two conversions write the halves of the
+// word themselves; through the 16-bit intrinsic each pair took further masks.)
 template <int FMT>
-__device__ __forceinline__ uint32_t encode2(float2 v) {
-  return static_cast<uint32_t>(
-      __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, FMT == BSGEMM_FP8_E5M2 ? __NV_E5M2 : __NV_E4M3));
+__device__ __forceinline__ uint32_t encode4(float2 a, float2 b) {
+  uint32_t r;
+  if constexpr (FMT == BSGEMM_FP8_E5M2)
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  else
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// Stores the codes of a run of quotients.
+template <int FMT>
+__device__ __forceinline__ void store_codes(uint8_t* q, const float2 (&v)[4]) {
+  *reinterpret_cast<uint2*>(q) = make_uint2(encode4<FMT>(v[0], v[1]), encode4<FMT>(v[2], v[3]));
 }
 
 // Stores the codes of v / s. The quotient is v times the reciprocal of s:
@@ -150,21 +179,25 @@ __device__ __forceinline__ uint32_t encode2(float2 v) {
 // that far from the exact one, against a code's half step of 2^-4.
 template <int FMT>
 __device__ __forceinline__ void store_codes(uint8_t* q, const float2 (&v)[4], const Scale& s) {
-  uint32_t c[4];
+  float2 d[4];
   if (s.rcp > 0.f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = encode2<FMT>(mul2(v[i], both(s.rcp)));
+    for (int i = 0; i < 4; ++i) d[i] = mul2(v[i], both(s.rcp));
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = encode2<FMT>(make_float2(__fdiv_rn(v[i].x, s.s), __fdiv_rn(v[i].y, s.s)));
+    for (int i = 0; i < 4; ++i) d[i] = make_float2(__fdiv_rn(v[i].x, s.s), __fdiv_rn(v[i].y, s.s));
   }
-  *reinterpret_cast<uint2*>(q) = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+  store_codes<FMT>(q, d);
 }
 
-// Larger of a and the run's magnitudes; NaNs are passed over.
+// Largest of a (not negative) and the run's magnitudes, two values to an
+// instruction; NaNs are passed over.
 __device__ __forceinline__ float max_abs(float a, const float2 (&v)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+  for (int i = 0; i < 4; ++i) {
+    const float b = a;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(b), "f"(v[i].x), "f"(v[i].y));
+  }
   return a;
 }
 

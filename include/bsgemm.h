@@ -309,7 +309,7 @@ bsgemm_status bsgemm_fp8_gemm_residual(int layout, int a_format, int b_format, c
  *                read it.
  *   weight       [cols] of weight_dtype (bsgemm_src_dtype)
  *   eps          finite, > 0
- *   rstd         FP32 [rows], or NULL: kept for the backward pass
+ *   rstd         FP32 [rows], for the backward pass
  * A row of values past 2^56 in magnitude may overflow its sum of squares
  * (rstd is then 0, and so is y). */
 bsgemm_status bsgemm_rms_norm_quantize_fp8(int src_dtype, int weight_dtype, int fp8_format,
