@@ -3,6 +3,10 @@
 Argument marshalling only: every step of the GEMM runs in ``libbsgemm.so``'s
 CUDA kernels.  PyTorch supplies device memory and streams.  There is no CPU
 path: if the library is missing (and cannot be built here) every call raises.
+The usual calls are marshalled in C++ (``_bsgemm_torch``, csrc/bsgemm_torch.cpp),
+which takes a third of the host time; what it does not take (outputs given, a
+stream given, another device, arguments to be refused) goes through the Python
+code here.
 
     out = bsgemm_fp8_nt(a, b, scale_a, scale_b)          # a [M,K], b [N,K]
     out = gemm(a, b, scale_a, scale_b, layout="tn")      # a [K,M], b [K,N]
@@ -31,6 +35,10 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported granularity", 3: "misa
 
 _lock = threading.Lock()
 _lib = None
+_fast = None    # the C++ marshalling, bound to the library's entry points by lib()
+_FAST_ENTRIES = ("bsgemm_fp8_gemm_fused", "bsgemm_fp8_gemm_residual", "bsgemm_rms_norm_quantize_fp8",
+                 "bsgemm_rms_norm_backward", "bsgemm_rms_norm_backward_workspace", "bsgemm_activation_quantize_fp8",
+                 "bsgemm_activation_backward_quantize_fp8", "bsgemm_activation_backward_workspace")
 
 
 class BsgemmError(RuntimeError):
@@ -73,7 +81,7 @@ EXPORTS = ("bsgemm_fp8_nt", "bsgemm_fp8_tn", "bsgemm_fp8_nn", "bsgemm_fp8_tt", "
 
 def lib():
     """Load ``libbsgemm.so`` (building it first if it is missing and nvcc exists)."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     with _lock:
@@ -81,6 +89,9 @@ def lib():
             if not os.path.exists(LIB_PATH):
                 from . import build as _build
                 _build.build()
+            if not os.path.exists(os.path.join(_HERE, "_bsgemm_torch.so")):
+                from . import build as _build
+                _build.build_binding()
             L = ctypes.CDLL(LIB_PATH)
             p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
             gemm_args = [p, p, p, p, p, i64, i64, i64, i32, p]
@@ -133,8 +144,25 @@ def lib():
             L.bsgemm_activation_backward_workspace.restype = size
             L.bsgemm_version.argtypes = []
             L.bsgemm_version.restype = i32
+            from . import _bsgemm_torch
+            _bsgemm_torch.bind(*(ctypes.cast(getattr(L, name), p).value for name in _FAST_ENTRIES))
+            _fast = _bsgemm_torch
             _lib = L
     return _lib
+
+
+def _marshal():
+    """The C++ marshalling, with the library loaded; None where it is switched off."""
+    if _lib is None:
+        lib()
+    return _fast
+
+
+def _taken(result, what: str):
+    """A result of the C++ marshalling: its outputs, or its status raised."""
+    if isinstance(result, int):
+        raise BsgemmError(result, what)
+    return result
 
 
 def status_string(status: int) -> str:
@@ -228,6 +256,13 @@ def gemm(a, b, scale_a, scale_b, out=None, layout="nt", gran=128, tuning=None, s
     [M, N] tensor of ``out_dtype`` or None; ``out`` may be ``residual`` itself."""
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
+    if out is None and tuning is None and stream is None and a_format is None and b_format is None and \
+            activation in ACTIVATIONS and (out_dtype is torch.bfloat16 or out_dtype is torch.float32):
+        fast = _marshal()
+        r = fast and fast.gemm(LAYOUTS[layout], gran, a, b, scale_a, scale_b, bias, ACTIVATIONS[activation],
+                               out_dtype is torch.float32, residual)
+        if r is not None:
+            return r if r.__class__ is torch.Tensor else _taken(r, f"bsgemm {layout} {a.shape} {b.shape} g={gran}")
     fa = _format(a, a_format, "a")
     fb = _format(b, b_format, "b")
     a = _as_bytes(a, "a")
@@ -389,6 +424,15 @@ def rms_norm_quantize(x, weight, residual=None, eps=1e-6, gran=128, fmt="e4m3", 
     the FP32 [rows] 1 / sqrt(mean(h^2) + eps), which ``rms_norm_backward``
     takes. ``residual_out`` (h's buffer) may be ``x`` or ``residual``. See
     ``bsgemm_rms_norm_quantize_fp8``."""
+    if q is None and scales is None and residual_out is None and stream is None and fmt in FORMATS:
+        fast = _marshal()
+        r = fast and fast.norm(x, weight, residual, eps, gran, FORMATS[fmt])
+        if r is not None:
+            if r.__class__ is not tuple:
+                _taken(r, f"bsgemm_rms_norm_quantize_fp8 {tuple(x.shape)} g={gran}")
+            q, scales, h, rstd = r
+            h = x if residual is None else h
+            return (q, scales, h, rstd) if return_rstd else (q, scales, h)
     _matrix(x, "x")
     dev, (rows, cols) = x.device, x.shape
     weight = _weight(weight, "weight", cols, dev)
@@ -423,6 +467,11 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual=None, dx=None, dweight=None
     or None; all matrices of one type. Returns (dx, dweight): the gradient of x
     and of the residual alike, and the FP32 [cols] gradient of the weight.
     ``dx`` may be ``dy`` or ``dresidual``. See ``bsgemm_rms_norm_backward``."""
+    if dx is None and dweight is None and stream is None:
+        fast = _marshal()
+        r = fast and fast.norm_backward(dy, h, weight, rstd, dresidual)
+        if r is not None:
+            return r if r.__class__ is tuple else _taken(r, f"bsgemm_rms_norm_backward {tuple(dy.shape)}")
     _matrix(dy, "dy")
     dev, (rows, cols) = dy.device, dy.shape
     _matrix(h, "h", dy.dtype, dev, dy.shape)
@@ -452,6 +501,12 @@ def activation_quantize(z, activation, gran=128, fmt="e4m3", q=None, scales=None
     """FP8 codes and block scales of activation(z), z an FP32 or BF16 [rows, cols]
     product with its bias; ``activation`` "relu" or "gelu" (without one,
     ``quantize``). Returns (q, scales). See ``bsgemm_activation_quantize_fp8``."""
+    if q is None and scales is None and stream is None and fmt in FORMATS and activation in ACTIVATIONS:
+        fast = _marshal()
+        r = fast and fast.act(z, ACTIVATIONS[activation], gran, FORMATS[fmt])
+        if r is not None:
+            return r if r.__class__ is tuple else \
+                _taken(r, f"bsgemm_activation_quantize_fp8 {tuple(z.shape)} g={gran} {activation}")
     _matrix(z, "z")
     act = _given_activation(activation)
     if fmt not in FORMATS:
@@ -475,6 +530,13 @@ def activation_backward_quantize(dout, z, activation=None, gran=128, fmt="e4m3",
     None or "none") are of one type. Returns (q, scales, dbias): one operand for
     both gradient products, and the FP32 [cols] column sums of dz (None with
     ``bias_grad=False``). See ``bsgemm_activation_backward_quantize_fp8``."""
+    if q is None and scales is None and dbias is None and stream is None and fmt in FORMATS and \
+            activation in ACTIVATIONS:
+        fast = _marshal()
+        r = fast and fast.act_backward(dout, z, ACTIVATIONS[activation], gran, FORMATS[fmt], bias_grad)
+        if r is not None:
+            return r if r.__class__ is tuple else \
+                _taken(r, f"bsgemm_activation_backward_quantize_fp8 {tuple(dout.shape)} g={gran} {activation}")
     _matrix(dout, "dout")
     act = _given_activation(activation)
     dev, (rows, cols) = dout.device, dout.shape

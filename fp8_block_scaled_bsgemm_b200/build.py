@@ -6,7 +6,9 @@ norm and activation kernels around the GEMM (``csrc/bsgemm_norm.cu``,
 ``csrc/bsgemm_act.cu``) and two kernel-instance units per
 (granularity, layout) pair (``csrc/bsgemm_inst.cu`` compiled with
 -DBSG_GRAN / -DBSG_LAYOUT, with and without -DBSG_RES=1) are compiled in
-parallel and linked into one shared library next to this file.  Objects are rebuilt only when a source under
+parallel and linked into one shared library next to this file, and the Python
+binding's marshalling module (``csrc/bsgemm_torch.cpp``) with g++ against the
+installed torch beside it.  Objects are rebuilt only when a source under
 ``csrc/`` or ``include/`` is newer than they are.
 
     python -m fp8_block_scaled_bsgemm_b200.build [--force] [-j N]
@@ -27,6 +29,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsgemm.so")
+BINDING_SRC = os.path.join(CSRC, "bsgemm_torch.cpp")
+BINDING = os.path.join(PKG, "_bsgemm_torch.so")
 
 GRANS = (64, 128, 256)
 LAYOUTS = ("nt", "tn", "nn", "tt")
@@ -44,7 +48,8 @@ def nvcc() -> str:
 
 
 def _newest_source() -> float:
-    files = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    files = [f for f in glob.glob(os.path.join(CSRC, "*")) if f != BINDING_SRC] + \
+        glob.glob(os.path.join(INCLUDE, "*.h"))
     return max(os.path.getmtime(f) for f in files)
 
 
@@ -58,6 +63,30 @@ def _compile(src: str, obj: str, defines: list[str]) -> str:
         raise RuntimeError(f"nvcc failed for {os.path.basename(obj)}:\n{r.stderr[-4000:]}")
     os.replace(obj + ".tmp", obj)
     return obj
+
+
+def build_binding(force: bool = False) -> str:
+    """The marshalling module, rebuilt when its source, the header or torch is newer."""
+    import sysconfig
+
+    import torch
+    sources = [BINDING_SRC, os.path.join(INCLUDE, "bsgemm.h"), torch.__file__]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, sources)):
+        return BINDING
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + ["-I" + i for i in includes] + \
+        [BINDING_SRC, "-o", tmp, "-L" + os.path.join(root, "lib")] + \
+        ["-l" + lib for lib in ("c10", "c10_cuda", "torch_cpu", "torch_cuda", "torch", "torch_python")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for bsgemm_torch.cpp:\n" + r.stderr[-4000:])
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
@@ -92,6 +121,7 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stderr[-4000:])
         os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 

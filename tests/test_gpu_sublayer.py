@@ -429,6 +429,37 @@ def test_graphs():
         assert all(torch.equal(u, v) for u, v in zip(got, want))
 
 
+def test_both_marshallings_agree(monkeypatch):
+    """The C++ marshalling takes the usual calls, and gives what the Python code gives."""
+    run = all_calls(gen_of(14))
+    assert bsg._marshal() is not None
+    want = run()
+    monkeypatch.setattr(bsg, "_fast", None)
+    got = run()
+    assert len(got) == len(want)
+    for u, v in zip(got, want):
+        assert u.dtype == v.dtype and u.shape == v.shape and torch.equal(u, v)
+    gen = gen_of(15)
+    a, b, sa, sb, _, _ = gemm_inputs(gen, 48, 272, 144, "tn", 64, "e5m2")
+    a = a.view(torch.float8_e5m2)
+    bias, res = randn(gen, 272), randn(gen, 48, 272)
+    kw = dict(layout="tn", gran=64, bias=bias, activation="gelu", out_dtype=torch.float32, residual=res)
+    slow = bsg.gemm(a, b, sa, sb, **kw)
+    monkeypatch.undo()
+    assert torch.equal(bsg.gemm(a, b, sa, sb, **kw), slow)
+    # what the C++ code leaves to the Python code: given outputs, views, other types
+    fast = bsg._marshal()
+    x, w = randn(gen, 64, 64), randn(gen, 64)
+    for bad in (x.t(), x[0], x.half(), x.cpu(), None, 3, x[:0]):
+        assert fast.norm(bad, w, None, 1e-6, 128, 0) is None
+    assert fast.norm(x, w[:3], None, 1e-6, 128, 0) is None and fast.norm(x, w, x[:3], 1e-6, 128, 0) is None
+    assert fast.norm(x, w, None, "eps", 128, 0) is None and fast.norm(x, w, None, 1e-6, 100, 0) is None
+    assert fast.norm(x, w, None, -1.0, 128, 0) == 1      # a status of the library's
+    assert fast.act(x, 0, 128, 0) == 1 and fast.act_backward(x, x, 0, 128, 0, True) is None
+    assert fast.norm_backward(x, x, w, w.double(), None) is None
+    assert fast.gemm(0, 128, x, x, w, w, None, 0, False, None) is None
+
+
 # ------------------------------------------------------------------ a sublayer
 
 
