@@ -5,7 +5,7 @@ The C ABI unit (``csrc/bsgemm_api.cu``), the allocation-free entry point
 norm and activation kernels around the GEMM (``csrc/bsgemm_norm.cu``,
 ``csrc/bsgemm_act.cu``) and two kernel-instance units per
 (granularity, layout) pair (``csrc/bsgemm_inst.cu`` compiled with
--DBSG_GRAN / -DBSG_LAYOUT, with and without -DBSG_RES=1) are compiled in
+-DBSG_GRAN / -DBSG_LAYOUT, with and without -DBSG_EPI=1) are compiled in
 parallel and linked into one shared library next to this file, and the Python
 binding's marshalling module (``csrc/bsgemm_torch.cpp``) with g++ against the
 installed torch beside it.  Objects are rebuilt only when a source under
@@ -102,10 +102,10 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
             units.append((os.path.join(CSRC, "bsgemm_inst.cu"),
                           os.path.join(BUILD, f"bsgemm_inst_g{g}_{lay}.o"),
                           [f"-DBSG_GRAN={g}", f"-DBSG_LAYOUT={lay}"]))
-            # the instances that add a residual
+            # the instances with an epilogue
             units.append((os.path.join(CSRC, "bsgemm_inst.cu"),
-                          os.path.join(BUILD, f"bsgemm_inst_res_g{g}_{lay}.o"),
-                          [f"-DBSG_GRAN={g}", f"-DBSG_LAYOUT={lay}", "-DBSG_RES=1"]))
+                          os.path.join(BUILD, f"bsgemm_inst_epi_g{g}_{lay}.o"),
+                          [f"-DBSG_GRAN={g}", f"-DBSG_LAYOUT={lay}", "-DBSG_EPI=1"]))
     todo = [u for u in units if force or not os.path.exists(u[1]) or os.path.getmtime(u[1]) < newest]
     if todo:
         jobs = jobs or max(1, min(len(todo), os.cpu_count() or 1))

@@ -426,8 +426,9 @@ bsgemm_status gemm_call(int layout, int a_format, int b_format, const void* a, c
   if (st != BSGEMM_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
+  const bool epilogue = opts.bias || opts.residual || (opts.epi & 3) != 0;
 #define BSG_RUN(G, L)                                                                            \
-  (residual ? bsg_host::run_res_g##G##_##L(pl, a, b, scale_a, scale_b, out, m, n, k, opts, s, dev) \
+  (epilogue ? bsg_host::run_epi_g##G##_##L(pl, a, b, scale_a, scale_b, out, m, n, k, opts, s, dev) \
             : bsg_host::run_g##G##_##L(pl, a, b, scale_a, scale_b, out, m, n, k, opts, s, dev))
 #define BSG_RUN_LAYOUTS(G)                              \
   switch (layout) {                                     \

@@ -74,7 +74,7 @@ struct CallOpts {
   int a_fmt = BSGEMM_FP8_E4M3;   // bsgemm_fp8_format of the logical A operand
   int b_fmt = BSGEMM_FP8_E4M3;   // ... and of B
   const float* bias = nullptr;   // FP32 [N] or null
-  const void* residual = nullptr; // [M, N] of the output's type, or null (run_res_* alone take one)
+  const void* residual = nullptr; // [M, N] of the output's type, or null (run_epi_* alone take one, and a bias or an activation)
   int epi = 0;                   // activation (bits 0-1) | FP32 output (bit 2)
   const int* group_m = nullptr;  // grouped GEMM: device rows per group
   int num_groups = 0;
@@ -84,7 +84,7 @@ struct CallOpts {
   bsgemm_status run_g##G##_##L(const bsgemm_plan& plan, const void* a, const void* b,          \
                                const float* sa, const float* sb, void* out, int M, int N, int K, \
                                const CallOpts& opts, cudaStream_t stream, const DeviceInfo& dev); \
-  bsgemm_status run_res_g##G##_##L(const bsgemm_plan& plan, const void* a, const void* b,      \
+  bsgemm_status run_epi_g##G##_##L(const bsgemm_plan& plan, const void* a, const void* b,      \
                                    const float* sa, const float* sb, void* out, int M, int N,   \
                                    int K, const CallOpts& opts, cudaStream_t stream,            \
                                    const DeviceInfo& dev);

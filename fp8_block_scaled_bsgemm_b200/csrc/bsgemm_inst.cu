@@ -1,7 +1,8 @@
 // Kernel instances and launch code for one (granularity, layout) pair.
 // The build compiles this file twice per pair with -DBSG_GRAN=<64|128|256>
-// and -DBSG_LAYOUT=<nt|tn|nn|tt>, the second time with -DBSG_RES=1 for the
-// instances that add a residual, so the twenty-four units build in parallel.
+// and -DBSG_LAYOUT=<nt|tn|nn|tt>, the second time with -DBSG_EPI=1 for the
+// instances with an epilogue (bias, activation, residual), so the twenty-four
+// units build in parallel.
 #include <cstring>
 
 #include "bsgemm_host.h"
@@ -15,13 +16,13 @@
 #error "compile with -DBSG_LAYOUT=nt|tn|nn|tt"
 #endif
 
-#ifndef BSG_RES
-#define BSG_RES 0
+#ifndef BSG_EPI
+#define BSG_EPI 0
 #endif
 
 #define BSG_CAT2(a, b, c, d) a##b##_##c
-#if BSG_RES
-#define BSG_RUN_NAME(G, L) BSG_CAT2(run_res_g, G, L, )
+#if BSG_EPI
+#define BSG_RUN_NAME(G, L) BSG_CAT2(run_epi_g, G, L, )
 #else
 #define BSG_RUN_NAME(G, L) BSG_CAT2(run_g, G, L, )
 #endif
@@ -35,7 +36,7 @@ namespace {
 constexpr const char* kLayout = BSG_STR(BSG_LAYOUT);
 constexpr bool kAMn = kLayout[0] == 't';
 constexpr bool kBMn = kLayout[1] == 'n';
-constexpr bool kRes = BSG_RES != 0;
+constexpr bool kEpi = BSG_EPI != 0;
 
 // Format fields of the instruction descriptor for operands P (MMA A side)
 // and Q (MMA B side).
@@ -48,7 +49,7 @@ bsgemm_status launch(const bsgemm_plan& plan, const void* a, const void* b, cons
                      const float* sb, void* out, int M, int N, int K, const CallOpts& opts,
                      cudaStream_t stream, const DeviceInfo& dev) {
   using SC = bsg::StageCfg<BNQ, Q_MN, SWAP, GROUPED>;
-  auto kern = bsg::bsgemm_kernel<BNQ, GRAN, SWAP, P_MN, Q_MN, SPLIT, GROUPED, kRes>;
+  auto kern = bsg::bsgemm_kernel<BNQ, GRAN, SWAP, P_MN, Q_MN, SPLIT, GROUPED, kEpi>;
 
   // P/Q operands: normally P = A (M rows), Q = B (N rows); swapped P = B, Q = A
   const void* p_ptr = SWAP ? b : a;
@@ -66,6 +67,10 @@ bsgemm_status launch(const bsgemm_plan& plan, const void* a, const void* b, cons
   std::memset(&tm_out, 0, sizeof tm_out);
   if (SC::kTmaStore) ok &= make_out_map(&tm_out, out, M, N, (opts.epi & bsg::kEpiOutF32) != 0);
   if (SC::kSwapTmaStore && !(opts.epi & bsg::kEpiOutF32)) ok &= make_swap_out_map(&tm_out, out, M, N, BNQ);
+  // the residual is read in the output's boxes (swap-AB tiles with plain loads)
+  CUtensorMap tm_res = tm_out;
+  if (kEpi && !SWAP && opts.residual)
+    ok &= make_out_map(&tm_res, const_cast<void*>(opts.residual), M, N, (opts.epi & bsg::kEpiOutF32) != 0);
   if (!ok) return BSGEMM_ERR_CUDA;
 
   bsg::Params prm{};
@@ -133,7 +138,7 @@ bsgemm_status launch(const bsgemm_plan& plan, const void* a, const void* b, cons
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, tm_p, tm_q, tm_out, prm) != cudaSuccess) return BSGEMM_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, tm_p, tm_q, tm_out, tm_res, prm) != cudaSuccess) return BSGEMM_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? BSGEMM_OK : BSGEMM_ERR_CUDA;
 }
 
@@ -143,7 +148,7 @@ bsgemm_status launch_pair(const bsgemm_plan& plan, const void* a, const void* b,
                           const float* sb, void* out, int M, int N, int K, const CallOpts& opts,
                           cudaStream_t stream, const DeviceInfo& dev) {
   using PC = bsg::PairCfg;
-  auto kern = bsg::bsgemm_pair_kernel<GRAN, P_MN, Q_MN, kRes>;
+  auto kern = bsg::bsgemm_pair_kernel<GRAN, P_MN, Q_MN, kEpi>;
   CUtensorMap tm_p, tm_q;
   bool ok = true;
   if (P_MN) ok &= make_map_2d(&tm_p, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, M, K, M, 128, bsg::BK);
@@ -152,6 +157,8 @@ bsgemm_status launch_pair(const bsgemm_plan& plan, const void* a, const void* b,
   else      ok &= make_map_2d(&tm_q, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, K, N, K, bsg::BK, bsg::kPairQRows);
   CUtensorMap tm_out;
   ok &= make_out_map(&tm_out, out, M, N, (opts.epi & bsg::kEpiOutF32) != 0);
+  CUtensorMap tm_res = tm_out;   // the residual is read in the output's boxes
+  if (kEpi && opts.residual) ok &= make_out_map(&tm_res, const_cast<void*>(opts.residual), M, N, (opts.epi & bsg::kEpiOutF32) != 0);
   if (!ok) return BSGEMM_ERR_CUDA;
 
   bsg::Params prm{};
@@ -217,7 +224,7 @@ bsgemm_status launch_pair(const bsgemm_plan& plan, const void* a, const void* b,
   if (pairs > max_pairs) pairs = max_pairs;
   if (pairs < 1) return BSGEMM_ERR_INVALID_ARG;
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  if (cudaLaunchKernelEx(&cfg, kern, tm_p, tm_q, tm_out, prm) != cudaSuccess) return BSGEMM_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, tm_p, tm_q, tm_out, tm_res, prm) != cudaSuccess) return BSGEMM_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? BSGEMM_OK : BSGEMM_ERR_CUDA;
 }
 
@@ -229,8 +236,8 @@ bsgemm_status BSG_RUN_NAME(BSG_GRAN, BSG_LAYOUT)(const bsgemm_plan& pl, const vo
                                                  const DeviceInfo& d) {
   constexpr int G = BSG_GRAN;
   if (pl.grouped) {
-    // grouped GEMM: NT only, whole tiles, no residual
-    if constexpr (!kAMn && !kBMn && !kRes) {
+    // grouped GEMM: NT only, whole tiles, no epilogue
+    if constexpr (!kAMn && !kBMn && !kEpi) {
       if (pl.bnq == 128) return launch<128, G, false, false, false, false, true>(pl, a, b, sa, sb, out, M, N, K, o, s, d);
       return launch<256, G, false, false, false, false, true>(pl, a, b, sa, sb, out, M, N, K, o, s, d);
     } else {

@@ -46,6 +46,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "bsgemm_gelu.cuh"
 #include "ptx.cuh"
 
 namespace bsg {
@@ -95,7 +96,7 @@ struct Params {
   int epi;               // epilogue: activation (bits 0-1: 0 none, 1 ReLU, 2 GELU), bit 2 FP32 output
   int num_groups;        // grouped GEMM: number of groups (0 otherwise)
   const float* bias;     // FP32 [N] added before the activation, or null
-  const void* residual;  // [M][N] in out's type, added after the activation (RES instances; may be out itself)
+  const void* residual;  // [M][N] in out's type, added after the activation, or null (may be out itself)
   const int* group_m;    // grouped GEMM: rows of each group (device, num_groups entries)
   const float* sP;       // [Pb][Kb]
   const float* sQ;       // [Qb][Kb]
@@ -130,11 +131,11 @@ struct StageCfg {
   static constexpr bool kTmaStore = !SWAP && !GROUPED;
   static constexpr bool kSwapTmaStore = SWAP;
   static constexpr int kEpiBytes = kTmaStore ? kNumEpiWarps * kEpiChunkBytes : (SWAP ? BNQ * BM * 2 : 0);
-  static constexpr int kBudget = 227 * 1024 - 1024 /*align slack*/ - 512 /*barriers*/;
+  static constexpr int kBudget = 227 * 1024 - 1024 /*align slack*/ - 640 /*barriers*/;
   static constexpr int kStagesRaw = (kBudget - kEpiBytes) / kStageBytes;
   static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
   static_assert(kStages >= 2, "shared memory too small for two stages");
-  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + 512;
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + 640;
 };
 
 struct __align__(8) Barriers {
@@ -147,11 +148,13 @@ struct __align__(8) Barriers {
   uint32_t tmem_base;
   int abort_flag;
   int split_last;
+  uint64_t residual[kNumEpiWarps];  // EPI: a chunk of the warp's residual has arrived
   // per promotion warp: the current work item's Pieces (pieces, slot,
   // counter, slot0, slot_base, slot_step), parked here for the K-loop
   int pieces[kNumEpiWarps][6];
 };
-static_assert(sizeof(Barriers) <= 512, "barrier block is 512 bytes");
+constexpr int kBarrierBytes = 640;
+static_assert(sizeof(Barriers) <= kBarrierBytes, "barrier block");
 
 // ---------------------------------------------------------------- helpers
 __device__ __forceinline__ void record_timeout(const Params& p, Barriers* bars, int where) {
@@ -436,12 +439,6 @@ __device__ __forceinline__ void stage_range(const Params& p, const Work& w, int&
 // 0.5 v (1 + erf(v / sqrt 2)).
 constexpr int kEpiRelu = 1, kEpiGelu = 2, kEpiOutF32 = 4;
 
-__device__ __forceinline__ float epi_act(float v, int act) {
-  if (act == kEpiRelu) return fmaxf(v, 0.f);
-  if (act == kEpiGelu) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-  return v;
-}
-
 template <int ACT>
 __device__ __forceinline__ float epi_act_t(float v) {
   if constexpr (ACT == kEpiRelu) return fmaxf(v, 0.f);
@@ -465,26 +462,6 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
   else f(ActTag<0>{});
 }
 
-// out = act(acc + bias[n]) in place on one thread's run of columns
-// [n0, n0 + 2 * NP) (acc pairs in column order).
-template <int NP>
-__device__ __forceinline__ void apply_epi(const Params& p, int n0, float2 (&acc)[NP]) {
-  const int act = p.epi & 3;
-  if (p.bias != nullptr || act != 0) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int n = n0 + 2 * i;
-      float b0 = 0.f, b1 = 0.f;
-      if (p.bias != nullptr && n < p.N) {
-        b0 = __ldg(p.bias + n);
-        b1 = __ldg(p.bias + n + 1);
-      }
-      acc[i].x = epi_act(acc[i].x + b0, act);
-      acc[i].y = epi_act(acc[i].y + b1, act);
-    }
-  }
-}
-
 __device__ __forceinline__ void st_shared_b16(uint32_t addr, unsigned short v) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
@@ -492,6 +469,10 @@ __device__ __forceinline__ void st_shared_b16(uint32_t addr, unsigned short v) {
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
+}
+
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
@@ -503,75 +484,236 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
-// acc += residual on the rows and columns of store_tile_tma (which follows).
-// A lane owns a row, and rows lie far apart, so the warp reads each chunk of
-// 32 rows x 128 bytes in memory order (8 lanes to a row's 128 bytes, four rows
-// to an instruction) and turns it through its staging buffer, in the same
-// swizzled places as the store. The loads go to L2 (ld.global.cg): out may be
-// the residual's own buffer. Every element is read by the warp that writes it,
-// before it writes it.
-template <int NP>
-__device__ __forceinline__ void add_residual(const Params& p, uint32_t buf, int m0, int n0, float2 (&acc)[NP],
-                                             uint32_t lane) {
-  if (m0 >= p.M) return;  // the warp's rows are all past the end
-  const uint32_t own = buf + lane * 128, sw = lane & 7;
-  const uint32_t piece = lane & 7;
-  auto chunks = [&](auto f32_tag) {
-    constexpr bool kF32 = decltype(f32_tag)::value != 0;
-    constexpr int kCols = kF32 ? 32 : 64;           // columns per chunk
-    constexpr int kChunks = 2 * NP / kCols;
-    constexpr size_t kElem = kF32 ? 4 : 2;
-    auto load = [&](int c, uint4 (&v)[8]) {
-      const int n = n0 + c * kCols + static_cast<int>(piece) * (kCols / 8);
+// acc = act(acc + bias[n]) on a warp's tile part, with its staging buffer (whose
+// last store it waits for): the bias of the warp's columns goes through the buffer, from which every lane
+// reads it as broadcast 16-byte words. Loaded per lane and column, the same
+// values cost 128 dependent loads a tile (8192 x 14336 x 4096 with bias: 784
+// against 473 us without). FAST_GELU: the one-exponential form, within 2e-7 of
+// the value that erff gives.
+template <int NP, bool FAST_GELU>
+__device__ __forceinline__ void apply_epi_staged(const Params& p, uint32_t buf, int n0, float2 (&acc)[NP], uint32_t lane) {
+  const int act = p.epi & 3;
+  if (p.bias != nullptr) {
+    float b[2 * NP / 32];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int m = m0 + 4 * i + static_cast<int>(lane >> 3);
-        v[i] = make_uint4(0, 0, 0, 0);
-        // N % 8 == 0: a 16-byte piece lies wholly inside the row or past it
-        if (m < p.M && n < p.N)
-          v[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.residual) +
-                                                       (static_cast<size_t>(m) * p.N + n) * kElem));
-      }
-    };
-    uint4 cur[8], nxt[8];
-    load(0, cur);
-    // the previous tile's store must have finished reading the buffer
+    for (int i = 0; i < 2 * NP / 32; ++i) {
+      const int n = n0 + 32 * i + static_cast<int>(lane);
+      b[i] = __ldg(p.bias + (n < p.N ? n : 0));
+    }
     if (lane == 0) bulk_wait_group_read0();
     __syncwarp();
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      if (c + 1 < kChunks) load(c + 1, nxt);
+    for (int i = 0; i < 2 * NP / 32; ++i) st_shared_f32(buf + (32 * i + lane) * 4, b[i]);
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t r = 4 * i + (lane >> 3);
-        st_shared_v4(buf + r * 128 + ((piece ^ (r & 7)) << 4), cur[i].x, cur[i].y, cur[i].z, cur[i].w);
+    for (int i = 0; i < NP / 2; ++i) {
+      const uint4 v = ld_shared_v4(buf + 16 * i);
+      acc[2 * i].x += __uint_as_float(v.x);
+      acc[2 * i].y += __uint_as_float(v.y);
+      acc[2 * i + 1].x += __uint_as_float(v.z);
+      acc[2 * i + 1].y += __uint_as_float(v.w);
+    }
+    __syncwarp();   // the buffer is read before it is written again
+  }
+  if (act == kEpiRelu) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) acc[i] = make_float2(fmaxf(acc[i].x, 0.f), fmaxf(acc[i].y, 0.f));
+  } else if (act == kEpiGelu) {
+    if constexpr (FAST_GELU) {
+#pragma unroll
+      for (int i = 0; i < NP; i += 4) {
+        float2 z[4], n[4], tail[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = acc[i + k];
+        bsgg::normal_tail(z, n, tail);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          acc[i + k] = ffma2(n[k], tail[k], make_float2(fmaxf(z[k].x, 0.f), fmaxf(z[k].y, 0.f)));
       }
-      __syncwarp();
+    } else {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint4 v = ld_shared_v4(own + ((u ^ sw) << 4));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        if constexpr (kF32) {
-          const int i = c * 16 + 2 * u;
-          acc[i].x += __uint_as_float(w[0]);
-          acc[i].y += __uint_as_float(w[1]);
-          acc[i + 1].x += __uint_as_float(w[2]);
-          acc[i + 1].y += __uint_as_float(w[3]);
-        } else {
+      for (int i = 0; i < NP; ++i)
+        acc[i] = make_float2(epi_act_t<kEpiGelu>(acc[i].x), epi_act_t<kEpiGelu>(acc[i].y));
+    }
+  }
+}
+
+// The residual of one promotion warp's part of a tile: rows [m0, m0 + 32),
+// columns [n0, n0 + 2 * NP), in chunks of 128 bytes a row, the staging buffer's
+// size and (swizzled) layout.
+//
+// The promotion warps pace the kernel, so whatever they wait for at a tile's
+// end is lost: reading the residual there with plain loads cost 2.8 us a tile
+// (4096^3, 17 us a tile), of which the loads' latency was 2. Instead the last
+// K-blocks' promotion covers the latency: some K-blocks before the end a TMA
+// load brings the first chunk into the warp's buffer (its last store has long
+// left it), and a few K-blocks later, without an activation, the chunk is added
+// to the accumulators and the next one is under way. With an activation the
+// first chunk waits in the buffer for the epilogue. Chunks that the K-loop had
+// no room for follow in the epilogue.
+// The sum is in FP32; a residual added early goes through the additions of
+// those last K-blocks too, at most kGap * kChunks of them.
+// Every element is read by the warp that writes it, before it writes it, so out
+// may be the residual's own buffer.
+struct ResidualState {
+  int next;       // K-block at which the next step is due (-1: none)
+  int started;    // chunks on their way or arrived
+  int added;      // chunks added
+  uint32_t phase; // of the warp's barrier
+};
+
+template <int NP, bool F32>
+struct ResidualChunks {
+  static constexpr int kCols = F32 ? 32 : 64;   // columns per chunk
+  static constexpr int kChunks = 2 * NP / kCols;
+
+  // the previous store must have finished reading the buffer, and every lane
+  // the chunk before this one
+  static __device__ __forceinline__ void start(const CUtensorMap* tm, uint32_t buf, uint32_t bar, int m0, int n0, int c,
+                                               uint32_t lane) {
+    if (lane == 0) {
+      bulk_wait_group_read0();
+      mbar_arrive_expect_tx(bar, kEpiChunkBytes);
+      tma_load_2d(buf, tm, bar, n0 + c * kCols, m0);
+    }
+    __syncwarp();
+  }
+  // the lane's own row of the buffer's chunk
+  static __device__ __forceinline__ void take(uint32_t buf, uint32_t lane, uint4 (&v)[8]) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            acc[c * 32 + 4 * u + k].x += __uint_as_float(w[k] << 16);
-            acc[c * 32 + 4 * u + k].y += __uint_as_float(w[k] & 0xFFFF0000u);
-          }
+    for (int u = 0; u < 8; ++u) v[u] = ld_shared_v4(buf + lane * 128 + ((u ^ (lane & 7)) << 4));
+    __syncwarp();
+  }
+  // acc += the lane's row of chunk C
+  template <int C>
+  static __device__ __forceinline__ void add(const uint4 (&v)[8], float2 (&acc)[NP]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      if constexpr (F32) {
+        const int i = C * 16 + 2 * u;
+        acc[i].x += __uint_as_float(w[0]);
+        acc[i].y += __uint_as_float(w[1]);
+        acc[i + 1].x += __uint_as_float(w[2]);
+        acc[i + 1].y += __uint_as_float(w[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc[C * 32 + 4 * u + k].x += __uint_as_float(w[k] << 16);
+          acc[C * 32 + 4 * u + k].y += __uint_as_float(w[k] & 0xFFFF0000u);
         }
       }
-      __syncwarp();   // every row is read before the next chunk, or the store, is written over it
-#pragma unroll
-      for (int i = 0; i < 8; ++i) cur[i] = nxt[i];
     }
-  };
-  if (p.epi & kEpiOutF32) chunks(ActTag<1>{});
-  else                    chunks(ActTag<0>{});
+  }
+  static __device__ __forceinline__ void add(int c, const uint4 (&v)[8], float2 (&acc)[NP]) {
+    if (c == 0) add<0>(v, acc);
+    if constexpr (kChunks > 1) {
+      if (c == 1) add<1>(v, acc);
+    }
+    if constexpr (kChunks > 2) {
+      if (c == 2) add<2>(v, acc);
+      if (c == 3) add<3>(v, acc);
+    }
+    static_assert(kChunks <= 4, "chunks are added by compile-time index");
+  }
+
+  // Waits for the chunk in the buffer, sends for the next one and adds it.
+  static __device__ __forceinline__ bool advance(const Params& p, Barriers* bars, const CUtensorMap* tm, uint32_t buf,
+                                                 uint32_t bar, int m0, int n0, ResidualState& s, float2 (&acc)[NP],
+                                                 uint32_t lane) {
+    if (!warp_wait_all(bar, s.phase, p, bars, 10)) return false;
+    s.phase ^= 1;
+    uint4 v[8];
+    take(buf, lane, v);
+    if (s.started < kChunks) start(tm, buf, bar, m0, n0, s.started++, lane);
+    add(s.added++, v, acc);
+    return true;
+  }
+
+  // A step in the K-loop.
+  static __device__ __forceinline__ bool step(const Params& p, Barriers* bars, const CUtensorMap* tm, uint32_t buf,
+                                              uint32_t bar, int m0, int n0, int gap, ResidualState& s,
+                                              float2 (&acc)[NP], uint32_t lane) {
+    if (s.started == 0) {
+      start(tm, buf, bar, m0, n0, 0, lane);
+      s.started = 1;
+      s.next = (p.epi & 3) == 0 ? s.next + gap : -1;
+      return true;
+    }
+    s.next = s.added + 1 < kChunks ? s.next + gap : -1;
+    return advance(p, bars, tm, buf, bar, m0, n0, s, acc, lane);
+  }
+
+  // The epilogue: what the K-loop left, the bias and the activation.
+  static __device__ __forceinline__ bool finish(const Params& p, Barriers* bars, const CUtensorMap* tm, uint32_t buf,
+                                                uint32_t bar, int m0, int n0, ResidualState& s, float2 (&acc)[NP],
+                                                uint32_t lane) {
+    if (p.residual == nullptr) {
+      apply_epi_staged<NP, false>(p, buf, n0, acc, lane);
+      return true;
+    }
+    if (s.started == 0) start(tm, buf, bar, m0, n0, s.started++, lane);
+    if ((p.epi & 3) == 0) {
+#pragma unroll 1
+      while (s.added < kChunks)
+        if (!advance(p, bars, tm, buf, bar, m0, n0, s, acc, lane)) return false;
+      apply_epi_staged<NP, true>(p, buf, n0, acc, lane);
+      return true;
+    }
+    // the residual comes after the activation: the first chunk moves to
+    // registers, since the bias goes through the buffer
+    if (!warp_wait_all(bar, s.phase, p, bars, 10)) return false;
+    s.phase ^= 1;
+    uint4 v[8];
+    take(buf, lane, v);
+    apply_epi_staged<NP, true>(p, buf, n0, acc, lane);
+    if constexpr (kChunks > 1) {
+      fence_proxy_async_smem();   // the bias's stores come before the load into the same buffer
+      start(tm, buf, bar, m0, n0, s.started++, lane);
+    }
+    add(s.added++, v, acc);
+#pragma unroll 1
+    while (s.added < kChunks)
+      if (!advance(p, bars, tm, buf, bar, m0, n0, s, acc, lane)) return false;
+    return true;
+  }
+};
+
+// Steps K-blocks apart, about two TMA latencies of promotion (0.5 us a K-block
+// of 128).
+template <int GRAN>
+constexpr int kResidualGap = GRAN == 64 ? 6 : GRAN == 128 ? 3 : 2;
+
+// The state at the start of an item with K-blocks [kb0, kb1): it steps in the
+// K-loop if it is known to store the tile (split-K's last piece is not).
+template <int NP, int GRAN>
+__device__ __forceinline__ void residual_begin(const Params& p, int kb0, int kb1, ResidualState& s) {
+  const int chunks = (p.epi & kEpiOutF32) ? ResidualChunks<NP, true>::kChunks : ResidualChunks<NP, false>::kChunks;
+  const int first = kb1 - kResidualGap<GRAN> * chunks;
+  s.started = s.added = 0;
+  s.next = p.residual != nullptr && kb0 == 0 && p.splits == 1 && kb1 > 1 ? (first > 1 ? first : 1) : -1;
+}
+
+template <int NP, int GRAN>
+__device__ __forceinline__ bool residual_step(const Params& p, Barriers* bars, const CUtensorMap* tm, uint32_t buf,
+                                              uint32_t bar, int m0, int n0, ResidualState& s, float2 (&acc)[NP],
+                                              uint32_t lane) {
+  return (p.epi & kEpiOutF32)
+             ? ResidualChunks<NP, true>::step(p, bars, tm, buf, bar, m0, n0, kResidualGap<GRAN>, s, acc, lane)
+             : ResidualChunks<NP, false>::step(p, bars, tm, buf, bar, m0, n0, kResidualGap<GRAN>, s, acc, lane);
+}
+
+template <int NP>
+__device__ __forceinline__ bool residual_finish(const Params& p, Barriers* bars, const CUtensorMap* tm, uint32_t buf,
+                                                uint32_t bar, int m0, int n0, ResidualState& s, float2 (&acc)[NP],
+                                                uint32_t lane) {
+  return (p.epi & kEpiOutF32) ? ResidualChunks<NP, true>::finish(p, bars, tm, buf, bar, m0, n0, s, acc, lane)
+                              : ResidualChunks<NP, false>::finish(p, bars, tm, buf, bar, m0, n0, s, acc, lane);
+}
+
+// After a wait gave up: a chunk still on its way lands before the warp leaves.
+__device__ __forceinline__ void residual_drain(const Params& p, Barriers* bars, uint32_t bar, const ResidualState& s) {
+  if (s.started > s.added) warp_wait_all(bar, s.phase, p, bars, 11, true);
 }
 
 // TMA-store epilogue of one promotion warp: lane l holds row m0 + l, columns
@@ -637,12 +779,10 @@ __device__ __forceinline__ void store_tile_tma(const Params& p, const CUtensorMa
 }
 
 // One thread's run of columns [n0, n0 + 2 * NP) of row m: acc pairs in
-// column order. Applies the epilogue in place and stores BF16 (8 per 16-byte
-// store) or FP32 (4 per 16-byte store); N % 8 == 0, so a group of 8 columns
+// column order. Stores BF16 (8 per 16-byte store) or FP32 (4 per 16-byte store); N % 8 == 0, so a group of 8 columns
 // is wholly inside or outside the matrix.
 template <int NP>
 __device__ __forceinline__ void store_row_run(const Params& p, int m, int n0, float2 (&acc)[NP]) {
-  apply_epi(p, n0, acc);
   if (p.epi & kEpiOutF32) {
     float* row = reinterpret_cast<float*>(p.out) + static_cast<size_t>(m) * p.N + n0;
 #pragma unroll
@@ -667,12 +807,14 @@ __device__ __forceinline__ void store_row_run(const Params& p, int m, int n0, fl
 }
 
 // ---------------------------------------------------------------- kernel
-// RES: the instance adds Params.residual (instances apart, so that the others
-// carry none of its code or registers).
-template <int BNQ, int GRAN, bool SWAP, bool P_MN, bool Q_MN, bool SPLIT, bool GROUPED = false, bool RES = false>
+// EPI: the instance has the epilogue's code: bias, activation, residual. The
+// others store the accumulators as they are; the activations' code alone, never
+// run, cost them 0.3 us a tile (4096^3: 71.5 against 73.1 us).
+template <int BNQ, int GRAN, bool SWAP, bool P_MN, bool Q_MN, bool SPLIT, bool GROUPED = false, bool EPI = false>
 __global__ void __launch_bounds__(kNumThreads, 1)
     bsgemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
-                  const __grid_constant__ CUtensorMap tm_out, const Params p) {
+                  const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_res,
+                  const Params p) {
   using TL = Tiles<BNQ, Q_MN>;
   using SC = StageCfg<BNQ, Q_MN, SWAP, GROUPED>;
   constexpr int STAGES = SC::kStages;
@@ -737,6 +879,9 @@ __global__ void __launch_bounds__(kNumThreads, 1)
     }
     mbar_init(smem_addr(&bars->mma_done), kIssuers);
     mbar_init(smem_addr(&bars->publish), kNumEpiWarps);
+    if constexpr (EPI) {
+      for (int w = 0; w < kNumEpiWarps; ++w) mbar_init(smem_addr(&bars->residual[w]), 1);
+    }
     bars->abort_flag = 0;
     bars->split_last = 0;
     fence_barrier_init();
@@ -1001,6 +1146,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
     uint32_t pc = 0;          // K-blocks consumed so far (TMEM buffer / phase)
     bool ok = true;
     float2 acc[kHalf / 2];    // this thread's row, columns [half*kHalf, (half+1)*kHalf)
+    ResidualState rstate{-1, 0, 0, 0};
 
     WorkIter wit;
     work_begin<SPLIT, GROUPED>(p, wit);
@@ -1018,6 +1164,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
         }
         __syncwarp();
       }
+      if constexpr (EPI && !SWAP) residual_begin<kHalf / 2, GRAN>(p, w.kb0, w.kb1, rstate);
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.f, 0.f);
 
@@ -1052,7 +1199,8 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       load_chunk(w.kb0, sc_cur);
       load_chunk(w.kb0 + 32, sc_nxt);
 
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++pc) {
+      // one K-block; false once a wait gave up
+      auto promote = [&](const int kb) -> bool {
         const int rel = kb - w.kb0;
         if (rel > 0 && (rel & 31) == 0) {
 #pragma unroll
@@ -1070,7 +1218,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
         // tcgen05.commit arrives only once the MMAs' TMEM writes are complete
         // every lane waits on the barrier itself: they all wake together when
         // the commit lands (a lane-0 wait plus a shuffle measured ~5 % slower)
-        if (!warp_wait_all(smem_addr(&bars->tmem_full[buf]), (pc / kBufs) & 1, p, bars, 4)) { ok = false; break; }
+        if (!warp_wait_all(smem_addr(&bars->tmem_full[buf]), (pc / kBufs) & 1, p, bars, 4)) return false;
         const uint32_t taddr = tmem_base + t_lane + buf * BNQ + half * kHalf;
         {
           // TMEM -> registers in chunks of up to 64 columns.  The buffer is
@@ -1095,6 +1243,26 @@ __global__ void __launch_bounds__(kNumThreads, 1)
                         acc[c * (CW / 2) + i]);
             }
           }
+        }
+        return true;
+      };
+      if constexpr (!EPI || SWAP) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++pc)
+          if (!promote(kb)) { ok = false; break; }
+      } else {
+        // in stretches between the residual's steps: with their code inside the
+        // loop it ran slower at every K-block (1.2 us a tile of 32)
+        for (int kb = w.kb0; ok && kb < w.kb1;) {
+          if (kb == rstate.next &&
+              !residual_step<kHalf / 2, GRAN>(p, bars, &tm_res, smem_addr(epi_bufs + ew * kEpiChunkBytes),
+                                              smem_addr(&bars->residual[ew]), w.tp * BM + quad * 32,
+                                              w.tq * BNQ + half * kHalf, rstate, acc, lane)) {
+            ok = false;
+            break;
+          }
+          const int stop = rstate.next > kb && rstate.next < w.kb1 ? rstate.next : w.kb1;
+          for (; kb < stop; ++kb, ++pc)
+            if (!promote(kb)) { ok = false; break; }
         }
       }
       if (!ok) break;
@@ -1194,22 +1362,32 @@ __global__ void __launch_bounds__(kNumThreads, 1)
         // tile rows are N, tile columns are M: out[m][n]
         const int n = w.tp * BM + row_in_tile;
         // the residual's elements of this thread, column n of rows m0 ..: a
-        // warp reads 32 consecutive n of a row at a time
-        float res[RES ? kHalf : 1];
-        if constexpr (RES) {
-          const int m0 = w.tq * BNQ + half * kHalf;
-          const size_t at = static_cast<size_t>(m0) * p.N + n;
+        // warp reads 32 consecutive n of a row at a time. Past the end the
+        // last row and column are read, and never stored: no load hangs on a
+        // condition.
+        float res[EPI ? kHalf : 1];
+        if constexpr (EPI) {
+          const int m0 = w.tq * BNQ + half * kHalf, last = p.M - 1;
+          const int nn = n < p.N ? n : p.N - 1;
+          auto load = [&](auto f32_tag) {
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i) {
-            res[i] = 0.f;
-            if (m0 + i < p.M && n < p.N) {
-              const size_t e = at + static_cast<size_t>(i) * p.N;
-              if (p.epi & kEpiOutF32)
+            for (int i = 0; i < kHalf; ++i) {
+              const size_t e = static_cast<size_t>(m0 + i < last ? m0 + i : last) * p.N + nn;
+              if constexpr (decltype(f32_tag)::value != 0)
                 res[i] = __ldcg(static_cast<const float*>(p.residual) + e);
               else
                 res[i] = __uint_as_float(
                     static_cast<uint32_t>(__ldcg(static_cast<const unsigned short*>(p.residual) + e)) << 16);
             }
+          };
+          if (p.residual == nullptr) {
+            // adding -0 leaves every value as it is
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) res[i] = -0.f;
+          } else if (p.epi & kEpiOutF32) {
+            load(ActTag<1>{});
+          } else {
+            load(ActTag<0>{});
           }
         }
         if (!(p.epi & kEpiOutF32)) {
@@ -1218,14 +1396,13 @@ __global__ void __launch_bounds__(kNumThreads, 1)
           // consecutive n (64 bytes); then one TMA copy stores the tile (rows
           // past M and columns past N are clipped by the tensor map)
           const uint32_t stage = smem_addr(epi_bufs);
-          const int act = p.epi & 3;
-          const float bn = (p.bias != nullptr && n < p.N) ? __ldg(p.bias + n) : 0.f;
           // the previous tile's store must have finished reading the buffer
           if (ew == 0 && lane == 0) bulk_wait_group_read0();
           named_barrier_sync(2, kNumEpiThreads);
           const uint32_t col0 = stage + (half * kHalf * BM + row_in_tile) * 2;  // m = half * kHalf
-          if constexpr (RES) {
-            with_act(act, [&](auto tag) {
+          if constexpr (EPI) {
+            const float bn = (p.bias != nullptr && n < p.N) ? __ldg(p.bias + n) : 0.f;
+            with_act(p.epi & 3, [&](auto tag) {
               constexpr int ACT = decltype(tag)::value;
 #pragma unroll
               for (int i = 0; i < kHalf; ++i) {
@@ -1233,24 +1410,13 @@ __global__ void __launch_bounds__(kNumThreads, 1)
                 st_shared_b16(col0 + i * BM * 2, __bfloat16_as_ushort(__float2bfloat16_rn(v)));
               }
             });
-          } else if (p.bias == nullptr && act == 0) {
-            // the plain BF16 output: no activation code in the loop (evaluated
-            // per element, the erf branch cost ~90 cycles a value)
+          } else {
 #pragma unroll
             for (int i = 0; i < kHalf / 2; ++i) {
               const __nv_bfloat162 h = __float22bfloat162_rn(acc[i]);
               st_shared_b16(col0 + (2 * i) * BM * 2, __bfloat16_as_ushort(h.x));
               st_shared_b16(col0 + (2 * i + 1) * BM * 2, __bfloat16_as_ushort(h.y));
             }
-          } else {
-            with_act(act, [&](auto tag) {
-              constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-              for (int i = 0; i < kHalf; ++i) {
-                const float v = epi_act_t<ACT>(((i & 1) ? acc[i / 2].y : acc[i / 2].x) + bn);
-                st_shared_b16(col0 + i * BM * 2, __bfloat16_as_ushort(__float2bfloat16_rn(v)));
-              }
-            });
           }
           fence_proxy_async_smem();
           named_barrier_sync(2, kNumEpiThreads);
@@ -1259,26 +1425,35 @@ __global__ void __launch_bounds__(kNumThreads, 1)
             bulk_commit_group();
           }
         } else if (n < p.N) {
-          const int act = p.epi & 3;
-          const float bn = p.bias != nullptr ? __ldg(p.bias + n) : 0.f;
-          with_act(act, [&](auto tag) {
-            constexpr int ACT = decltype(tag)::value;
+          auto store = [&](int i, float v) {
+            const int m = w.tq * BNQ + half * kHalf + i;
+            if (m < p.M) reinterpret_cast<float*>(p.out)[static_cast<size_t>(m) * p.N + n] = v;
+          };
+          if constexpr (EPI) {
+            const float bn = p.bias != nullptr ? __ldg(p.bias + n) : 0.f;
+            with_act(p.epi & 3, [&](auto tag) {
+              constexpr int ACT = decltype(tag)::value;
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) {
-              const int m = w.tq * BNQ + half * kHalf + i;
-              float v = epi_act_t<ACT>(((i & 1) ? acc[i / 2].y : acc[i / 2].x) + bn);
-              if constexpr (RES) v += res[i];
-              if (m < p.M) reinterpret_cast<float*>(p.out)[static_cast<size_t>(m) * p.N + n] = v;
-            }
-          });
+              for (int i = 0; i < kHalf; ++i)
+                store(i, epi_act_t<ACT>(((i & 1) ? acc[i / 2].y : acc[i / 2].x) + bn) + res[i]);
+            });
+          } else {
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) store(i, (i & 1) ? acc[i / 2].y : acc[i / 2].x);
+          }
         }
       } else if constexpr (SC::kTmaStore) {
         // this thread owns row m0 + lane, columns [n0, n0 + kHalf); the warp
         // stores its 32 rows through its staging buffer
         const int n0 = w.tq * BNQ + half * kHalf;
-        apply_epi<kHalf / 2>(p, n0, acc);
-        if constexpr (RES)
-          add_residual<kHalf / 2>(p, smem_addr(epi_bufs + ew * kEpiChunkBytes), w.tp * BM + quad * 32, n0, acc, lane);
+        if constexpr (EPI) {
+          if (!residual_finish<kHalf / 2>(p, bars, &tm_res, smem_addr(epi_bufs + ew * kEpiChunkBytes),
+                                          smem_addr(&bars->residual[ew]), w.tp * BM + quad * 32, n0, rstate, acc,
+                                          lane)) {
+            ok = false;
+            break;
+          }
+        }
         store_tile_tma<kHalf / 2>(p, &tm_out, smem_addr(epi_bufs + ew * kEpiChunkBytes),
                                   w.tp * BM + quad * 32, n0, acc, lane);
       } else {
@@ -1294,6 +1469,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
     if constexpr (SC::kTmaStore || SC::kSwapTmaStore) {
       if (lane == 0) bulk_wait_group0();
     }
+    if constexpr (EPI && !SWAP) residual_drain(p, bars, smem_addr(&bars->residual[ew]), rstate);
   }
   __syncwarp();
 

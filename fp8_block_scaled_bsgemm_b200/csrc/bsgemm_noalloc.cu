@@ -180,7 +180,7 @@ bsgemm_status launch_fixed(const bsgemm_plan& plan, const void* a, const void* b
       return BSGEMM_ERR_CUDA;
     setup.mark(d.ordinal);
   }
-  kern<<<plan.grid, bsg::kNumThreads, SC::kSmemBytes, stream>>>(tm_p, tm_q, tm_out, prm);
+  kern<<<plan.grid, bsg::kNumThreads, SC::kSmemBytes, stream>>>(tm_p, tm_q, tm_out, tm_out /* no residual */, prm);
   return cudaGetLastError() == cudaSuccess ? BSGEMM_OK : BSGEMM_ERR_CUDA;
 }
 

@@ -41,10 +41,10 @@ struct PairCfg {
   static constexpr int kQBytes = kPairQRows * BK;  // 16 KB
   static constexpr int kStageBytes = kPBytes + kQBytes;
   static constexpr int kEpiBytes = kNumEpiWarps * kEpiChunkBytes;  // 32 KB of store staging
-  static constexpr int kBudget = 227 * 1024 - 1024 /*align slack*/ - 512 /*barriers*/;
+  static constexpr int kBudget = 227 * 1024 - 1024 /*align slack*/ - kBarrierBytes;
   static constexpr int kStagesRaw = (kBudget - kEpiBytes) / kStageBytes;
   static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
-  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + 512;
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + kBarrierBytes;
 };
 
 template <bool P_MN, bool Q_MN>
@@ -58,11 +58,12 @@ __device__ __forceinline__ constexpr uint32_t instr_desc_pair() {
 
 // Whole 256 x 256 tiles only (no split-K / stream-K); Params.tiles_p and
 // tiles_q count pair tiles, Params.num_work is their number.
-// RES: the instance adds Params.residual, as in bsgemm_kernel.
-template <int GRAN, bool P_MN, bool Q_MN, bool RES = false>
+// EPI: the instance has the epilogue's code, as in bsgemm_kernel.
+template <int GRAN, bool P_MN, bool Q_MN, bool EPI = false>
 __global__ void __launch_bounds__(kNumThreads, 1)
     bsgemm_pair_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
-                       const __grid_constant__ CUtensorMap tm_out, const Params p) {
+                       const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_res,
+                       const Params p) {
   using PC = PairCfg;
   constexpr int STAGES = PC::kStages;
   constexpr int BNQ = kPairN;
@@ -107,6 +108,9 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       mbar_init(smem_addr(&bars->tmem_empty[b]), 2 * kNumEpiWarps);
     }
     mbar_init(smem_addr(&bars->mma_done), kIssuers);
+    if constexpr (EPI) {
+      for (int w = 0; w < kNumEpiWarps; ++w) mbar_init(smem_addr(&bars->residual[w]), 1);
+    }
     bars->abort_flag = 0;
     bars->split_last = 0;
     fence_barrier_init();
@@ -292,11 +296,13 @@ __global__ void __launch_bounds__(kNumThreads, 1)
     uint32_t pc = 0;
     bool ok = true;
     float2 acc[kHalf / 2];
+    ResidualState rstate{-1, 0, 0, 0};
 
     for (int t = cluster; t < p.num_work && ok; t += num_clusters) {
       int tp, tq;
       tile_coords(p, t, tp, tq);
       const int prow0 = tp * kPairM + static_cast<int>(rank) * BM;   // first P row of this CTA
+      if constexpr (EPI) residual_begin<kHalf / 2, GRAN>(p, 0, p.Kb, rstate);
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.f, 0.f);
 
@@ -321,7 +327,8 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       load_chunk(0, sc_cur);
       load_chunk(32, sc_nxt);
 
-      for (int kb = 0; kb < p.Kb; ++kb, ++pc) {
+      // one K-block; false once a wait gave up
+      auto promote = [&](const int kb) -> bool {
         if (kb > 0 && (kb & 31) == 0) {
 #pragma unroll
           for (int j = 0; j < kNumGroups; ++j) sc_cur[j] = sc_nxt[j];
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
         const uint32_t buf = pc % kBufs;
         // every lane waits on the barrier itself: they all wake together when
         // the commit lands (a lane-0 wait plus a shuffle measured ~5 % slower)
-        if (!warp_wait_all(smem_addr(&bars->tmem_full[buf]), (pc / kBufs) & 1, p, bars, 4)) { ok = false; break; }
+        if (!warp_wait_all(smem_addr(&bars->tmem_full[buf]), (pc / kBufs) & 1, p, bars, 4)) return false;
         const uint32_t taddr = tmem_base + t_lane + buf * BNQ + half * kHalf;
         {
           // 64-column chunks; the buffer is released (to the even CTA's
@@ -361,6 +368,25 @@ __global__ void __launch_bounds__(kNumThreads, 1)
             }
           }
         }
+        return true;
+      };
+      if constexpr (!EPI) {
+        for (int kb = 0; kb < p.Kb; ++kb, ++pc)
+          if (!promote(kb)) { ok = false; break; }
+      } else {
+        // in stretches between the residual's steps, as in bsgemm_kernel
+        for (int kb = 0; ok && kb < p.Kb;) {
+          if (kb == rstate.next &&
+              !residual_step<kHalf / 2, GRAN>(p, bars, &tm_res, smem_addr(epi_bufs + ew * kEpiChunkBytes),
+                                              smem_addr(&bars->residual[ew]), prow0 + quad * 32,
+                                              tq * kPairN + half * kHalf, rstate, acc, lane)) {
+            ok = false;
+            break;
+          }
+          const int stop = rstate.next > kb && rstate.next < p.Kb ? rstate.next : p.Kb;
+          for (; kb < stop; ++kb, ++pc)
+            if (!promote(kb)) { ok = false; break; }
+        }
       }
       if (!ok) break;
 
@@ -368,14 +394,19 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       // this thread owns row prow0 + row_in_tile, columns [n0, n0 + kHalf);
       // the warp stores its 32 rows through its staging buffer
       const int n0 = tq * kPairN + half * kHalf;
-      apply_epi<kHalf / 2>(p, n0, acc);
-      if constexpr (RES)
-        add_residual<kHalf / 2>(p, smem_addr(epi_bufs + ew * kEpiChunkBytes), prow0 + quad * 32, n0, acc, lane);
+      if constexpr (EPI) {
+        if (!residual_finish<kHalf / 2>(p, bars, &tm_res, smem_addr(epi_bufs + ew * kEpiChunkBytes),
+                                        smem_addr(&bars->residual[ew]), prow0 + quad * 32, n0, rstate, acc, lane)) {
+          ok = false;
+          break;
+        }
+      }
       store_tile_tma<kHalf / 2>(p, &tm_out, smem_addr(epi_bufs + ew * kEpiChunkBytes), prow0 + quad * 32, n0,
                                 acc, lane);
     }
     // every bulk store this warp issued has finished before the CTA exits
     if (lane == 0) bulk_wait_group0();
+    if constexpr (EPI) residual_drain(p, bars, smem_addr(&bars->residual[ew]), rstate);
   }
   __syncwarp();
 

@@ -117,10 +117,10 @@ def test_workspace_sizes():
     assert L.bsgemm_activation_backward_workspace(1 << 30, 1 << 20, 64) == (1 << 24) * (1 << 20) * 4
 
 
-def test_residual_instances_have_the_planned_launch_registers():
-    """The widest tiles' register split needs exactly 168 launch registers, in the residual's instances too."""
+def test_epilogue_instances_have_the_planned_launch_registers():
+    """The widest tiles' register split needs exactly 168 launch registers, in the epilogue's instances too."""
     bsg_build.build()
-    logs = glob.glob(os.path.join(ROOT, "_build", "bsgemm_inst_res_g*.log"))
+    logs = glob.glob(os.path.join(ROOT, "_build", "bsgemm_inst_epi_g*.log"))
     assert len(logs) == 12
     wide = 0
     for log in logs:
@@ -186,9 +186,9 @@ def test_fitted_gelu():
     one more for the exponential. GELU: that times |z|, 1.1e-7 + 4 U = 3.5e-7, and its own rounding. The slope adds
     u phi(u) <= 0.25 with (u^2 / 2 + 4) U of itself, below U, and three sums below 1.2: 5 U more, 6.5e-7.
     """
-    src = open(os.path.join(ROOT, "fp8_block_scaled_bsgemm_b200", "csrc", "bsgemm_act.cu")).read()
+    src = open(os.path.join(ROOT, "fp8_block_scaled_bsgemm_b200", "csrc", "bsgemm_gelu.cuh")).read()
     num = r"-?[\d.]+(?:e-\d+)?"
-    first = float(re.search(rf"t\[i\] = both\(({num})f\)", src).group(1))
+    first = float(re.search(rf"t\[i\] = both2\(({num})f\)", src).group(1))
     coef = [float(c.strip().rstrip("f")) for c in re.search(r"coef\[6\] = \{([^}]*)\}", src).group(1).split(",")]
     assert len(coef) == 6
     z = torch.linspace(-20, 20, 800001, dtype=torch.float64).float()
