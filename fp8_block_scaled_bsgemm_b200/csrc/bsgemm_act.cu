@@ -179,5 +179,5 @@ extern "C" bsgemm_status bsgemm_activation_backward_quantize_fp8(int src_dtype, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = bsga::run<bsga::Backward>(src_dtype, fp8_format, activation, gran, p, s, dev);
   if (st != BSGEMM_OK || need == 0) return st;
-  return bsgr::launch_column_sum(p.part, static_cast<int>(bsga::parts_of(rows, gran)), cols, dbias, s);
+  return bsgr::launch_column_sum(p.part, static_cast<int>(bsga::parts_of(rows, gran)), cols, dbias, s, dev);
 }

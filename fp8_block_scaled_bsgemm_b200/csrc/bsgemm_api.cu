@@ -390,6 +390,38 @@ extern "C" bsgemm_status bsgemm_make_plan(int layout, int64_t M, int64_t N, int6
 // ------------------------------------------------------------------ entry points
 namespace {
 
+// The automatic plan of a call with a residual, where it differs from the plain
+// call's: at g = 128 the epilogue's whole-tile instances promote faster than
+// their CTA pairs and stream-K instances, so those need a larger saving to pay.
+// Measured with a residual, g = 128 (us): stream-K against whole tiles, where it
+// saves 35 % of the busiest CTA's K-blocks 61 against 64 (1536 x 4096 x 8192),
+// where it saves 13 % 74 against 67 (2048 x 4096 x 8192) and 138 against 129
+// (4096 x 4096 x 8192), where it saves 0.4 % 469 against 430 (8192 x 4096 x
+// 14336); pairs against single CTAs 271 against 250 (2048 x 4096 x 32768). At
+// g = 64 stream-K stays ahead (114 against 122, 2048 x 4096 x 8192).
+bsgemm_status residual_plan(int layout, int64_t M, int64_t N, int64_t K, int gran, int num_sms, bsgemm_plan* pl) {
+  bsgemm_status st = bsgemm_make_plan(layout, M, N, K, gran, num_sms, nullptr, pl);
+  if (st != BSGEMM_OK || gran != 128) return st;
+  bsgemm_tuning t{};
+  if (pl->cta_pair) {
+    t.variant = BSGEMM_VARIANT_DATA_PARALLEL;
+    st = bsgemm_make_plan(layout, M, N, K, gran, num_sms, &t, pl);
+    if (st != BSGEMM_OK) return st;
+  }
+  if (pl->sk_ctas > 0 && pl->sk_first_tile > 0) {
+    const double waves = static_cast<double>(pl->sk_first_tile) / num_sms, U = pl->sk_units_per_tile;
+    const double whole = (waves + 1) * U;
+    const double split = waves * U + (pl->sk_units + pl->sk_ctas - 1) / pl->sk_ctas + 2.0 * (1.0 + pl->bnq / 128.0);
+    if (split > 0.8 * whole) {
+      t.variant = BSGEMM_VARIANT_DATA_PARALLEL;
+      t.bnq = pl->bnq;
+      t.stream_k = -1;
+      st = bsgemm_make_plan(layout, M, N, K, gran, num_sms, &t, pl);
+    }
+  }
+  return st;
+}
+
 bsgemm_status gemm_call(int layout, int a_format, int b_format, const void* a, const void* b,
                         const float* scale_a, const float* scale_b, const bsgemm_epilogue* epi,
                         const void* residual, void* out, int64_t M, int64_t N, int64_t K, int gran,
@@ -422,7 +454,8 @@ bsgemm_status gemm_call(int layout, int a_format, int b_format, const void* a, c
   st = device_info(dev);
   if (st != BSGEMM_OK) return st;
   bsgemm_plan pl;
-  st = bsgemm_make_plan(layout, M, N, K, gran, dev.num_sms, tuning, &pl);
+  st = residual && !tuning ? residual_plan(layout, M, N, K, gran, dev.num_sms, &pl)
+                           : bsgemm_make_plan(layout, M, N, K, gran, dev.num_sms, tuning, &pl);
   if (st != BSGEMM_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);

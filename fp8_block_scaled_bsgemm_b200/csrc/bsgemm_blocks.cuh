@@ -63,14 +63,18 @@ struct Walk {
 };
 
 // Copies a run into shared memory, zeros (and no access) where it lies outside
-// the matrix.
-template <bool BF16>
+// the matrix (WHOLE: it does not).
+template <bool BF16, bool WHOLE>
 __device__ __forceinline__ void fetch_run(uint32_t dst, const char* src, bool in) {
-  const int bytes = in ? 16 : 0;
 #pragma unroll
-  for (int h = 0; h < (BF16 ? 1 : 2); ++h)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * h), "l"(src + 16 * h), "r"(bytes)
-                 : "memory");
+  for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+    if constexpr (WHOLE)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * h), "l"(src + 16 * h) : "memory");
+    else
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * h), "l"(src + (in ? 16 * h : 0)),
+                   "r"(in ? 16 : 0)
+                   : "memory");
+  }
 }
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -104,16 +108,18 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
   const int part = static_cast<int>(blockIdx.x % P);   // the CTA's rank in its cluster
   const int row0 = part * (G / P) + tid / L;           // the thread's first row of a block
   const int col8 = (tid % L) * kVec;
-  const int64_t row_step = RP * p.cols;                // elements from one of the thread's rows to the next
-  const int cols = static_cast<int>(p.cols);           // at most 2^30
+  const int cols = static_cast<int>(p.cols);           // at most 2^24, rows at most 2^30
   const int rows = static_cast<int>(p.rows);
-
-  // the thread's first element in block w, and how many of its NP rows exist
-  auto place = [&](const Walk& w, int64_t& at) {
-    at = (static_cast<int64_t>(w.rb) * G + row0) * p.cols + static_cast<int64_t>(w.cb) * G + col8;
-    const int left = rows - w.rb * G - row0;           // rows + G stays below 2^31
-    return w.cb * G + col8 < cols ? left : 0;          // row j * RP of the thread exists if below this
-  };
+  // the thread's elements within a row of blocks: a block's first element is the
+  // same for all threads, and 256 rows of 2^24 columns are counted in 32 bits
+  uint32_t off[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) off[j] = static_cast<uint32_t>(row0 + j * RP) * cols + col8;
+  auto first_of = [&](const Walk& w) { return static_cast<int64_t>(w.rb) * G * p.cols + w.cb * G; };
+  // row j * RP of the thread exists in block w if below this
+  auto left_of = [&](const Walk& w) { return w.cb * G + col8 < cols ? rows - w.rb * G - row0 : 0; };
+  // the whole block lies inside the matrix
+  auto whole_of = [&](const Walk& w) { return (w.cb + 1) * G <= cols && rows - w.rb * G >= G; };
 
   bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
@@ -126,14 +132,24 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
   const char* in1 = static_cast<const char*>(p.in1);
   auto fetch = [&](const Walk& w, int buf) {
     if (w.rb < p.row_blocks) {
-      int64_t at;
-      const int left = place(w, at);
+      const int64_t first = first_of(w);
+      const char* src0 = in0 + first * kElem;
+      const char* src1 = in1 + (IN2 ? first * kElem : 0);
+      if (whole_of(w)) {
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const bool in = j * RP < left;
-        const int64_t e = in ? (at + j * row_step) * kElem : 0;
-        fetch_run<BF16>(slot(buf, 0, j), in0 + e, in);
-        if constexpr (IN2) fetch_run<BF16>(slot(buf, 1, j), in1 + e, in);
+        for (int j = 0; j < NP; ++j) {
+          fetch_run<BF16, true>(slot(buf, 0, j), src0 + static_cast<uint64_t>(off[j]) * kElem, true);
+          if constexpr (IN2) fetch_run<BF16, true>(slot(buf, 1, j), src1 + static_cast<uint64_t>(off[j]) * kElem, true);
+        }
+      } else {
+        const int left = left_of(w);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const bool in = j * RP < left;
+          const uint64_t e = in ? static_cast<uint64_t>(off[j]) * kElem : 0;
+          fetch_run<BF16, false>(slot(buf, 0, j), src0 + e, in);
+          if constexpr (IN2) fetch_run<BF16, false>(slot(buf, 1, j), src1 + e, in);
+        }
       }
     }
     fetch_commit();
@@ -153,8 +169,9 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
   if constexpr (kBuf > 0) fetch(w, 0);
   int par = 0;   // parity of the block: which copy of the exchanged values it uses
   for (; w.rb < p.row_blocks; par ^= 1) {
-    int64_t at;
-    const int left = place(w, at);
+    const int64_t first = first_of(w);
+    const int left = left_of(w);
+    const bool whole = whole_of(w);
     const int64_t blk = static_cast<int64_t>(w.rb) * p.col_blocks + w.cb;
     const int c0 = w.cb * G;
     const int64_t part_row = static_cast<int64_t>(w.rb) * P + part;
@@ -179,8 +196,8 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
       } else {
         a = b = zero_run<BF16>();
         if (j * RP < left) {
-          a = load_run<BF16>(in0, at + j * row_step);
-          if constexpr (IN2) b = load_run<BF16>(in1, at + j * row_step);
+          a = load_run<BF16>(in0, first + off[j]);
+          if constexpr (IN2) b = load_run<BF16>(in1, first + off[j]);
         }
       }
       float2 z[4];
@@ -226,9 +243,19 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
     }
     const Scale s = block_scale<FMT>(amax);
     if (tid == 0 && part == 0) p.scales[blk] = s.s;
+    uint8_t* q = p.q + first;
+    if (whole && s.rcp > 0.f) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
-      if (j * RP < left) store_codes<FMT>(p.q + at + j * row_step, v[j], s);
+      for (int j = 0; j < NP; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], both(s.rcp));
+        store_codes<FMT>(q + off[j], v[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        if (j * RP < left) store_codes<FMT>(q + off[j], v[j], s);
+    }
     if constexpr (SUMS) {
       if (p.part != nullptr && tid < G && c0 + tid < cols) {
         float sum = col_sum[par][0][tid];
@@ -247,13 +274,6 @@ template <int G, bool BF16, int FMT, typename Op>
 bsgemm_status launch_blocks(BlockParams& p, const Op& op, cudaStream_t stream, const bsg_host::DeviceInfo& dev) {
   constexpr bool IN2 = Op::kInputs == 2;
   constexpr int kSmem = kBufBytes<G, BF16, IN2> * kBufs<G, BF16, IN2>;
-  auto kern = block_quant_kernel<G, BF16, FMT, Op>;
-  static bsg_host::PerDeviceOnce setup;
-  if (!setup.done(dev.ordinal)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-      return BSGEMM_ERR_CUDA;
-    setup.mark(dev.ordinal);
-  }
   p.row_blocks = static_cast<int>((p.rows + G - 1) / G);
   p.col_blocks = static_cast<int>((p.cols + G - 1) / G);
   int64_t units = int64_t{dev.num_sms} * kCtasPerSm<G> / kParts<G>;   // blocks taken at the same time
@@ -261,7 +281,8 @@ bsgemm_status launch_blocks(BlockParams& p, const Op& op, cudaStream_t stream, c
   if (units > blocks) units = blocks;
   p.step_rb = static_cast<int>(units / p.col_blocks);
   p.step_cb = static_cast<int>(units % p.col_blocks);
-  return launch_rows(kern, units * kParts<G>, kThreads<G>, kSmem, kParts<G>, stream, p, op);
+  return launch_rows<block_quant_kernel<G, BF16, FMT, Op>>(dev, units * kParts<G>, kThreads<G>, kSmem, kParts<G>,
+                                                           stream, p, op);
 }
 
 // The same for run-time sizes and formats.

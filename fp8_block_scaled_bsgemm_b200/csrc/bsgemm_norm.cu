@@ -358,21 +358,13 @@ __global__ void __launch_bounds__(kFewThreads) norm_few_kernel(const __grid_cons
 
 template <int G, bool BF16, int FMT, bool RES>
 bsgemm_status launch_few(NormParams& p, cudaStream_t stream, const bsg_host::DeviceInfo& dev) {
-  auto kern = norm_few_kernel<G, BF16, FMT, RES>;
-  static bsg_host::PerDeviceOnce setup;
-  if (!setup.done(dev.ordinal)) {
-    // clusters of 16 are beyond the portable size
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-      return BSGEMM_ERR_CUDA;
-    setup.mark(dev.ordinal);
-  }
   p.col_blocks = static_cast<int>((p.cols + G - 1) / G);
   p.row_log = 0;
   while ((1 << p.row_log) < p.rows) ++p.row_log;
   // as many CTAs as have blocks for all their slots, at most 16
   p.cluster = 1;
   while (p.cluster < kMaxCluster && p.cluster * (kFewRows<G> >> p.row_log) < p.col_blocks) p.cluster *= 2;
-  return launch_rows(kern, p.cluster, kFewThreads, 0, p.cluster, stream, p);
+  return launch_rows<norm_few_kernel<G, BF16, FMT, RES>>(dev, p.cluster, kFewThreads, 0, p.cluster, stream, p);
 }
 
 template <int G, bool BF16, int FMT>
@@ -398,8 +390,9 @@ bsgemm_status norm_of(int fmt, int gran, NormParams& p, cudaStream_t st, const b
          (p.rows << p.tc_log) < int64_t{dev.num_sms} * 1024)
     ++p.tc_log;
   const int64_t per_cta = kRowThreads >> p.tc_log;
-  auto kern = p.residual ? norm_rows_kernel<BF16, true> : norm_rows_kernel<BF16, false>;
-  bsgemm_status s = launch_rows(kern, (p.rows + per_cta - 1) / per_cta, kRowThreads, 0, 1, st, p);
+  const int64_t ctas = (p.rows + per_cta - 1) / per_cta;
+  bsgemm_status s = p.residual ? launch_rows<norm_rows_kernel<BF16, true>>(dev, ctas, kRowThreads, 0, 1, st, p)
+                               : launch_rows<norm_rows_kernel<BF16, false>>(dev, ctas, kRowThreads, 0, 1, st, p);
   if (s != BSGEMM_OK) return s;
   BlockParams b{};
   b.in0 = p.residual ? p.stream_out : p.x;
@@ -413,20 +406,20 @@ bsgemm_status norm_of(int fmt, int gran, NormParams& p, cudaStream_t st, const b
 // ------------------------------------------------------------------ backward
 //
 // A row's gradient needs one sum over its columns (dy * weight * h), so a row
-// is read once into registers: a cluster of C CTAs takes the columns of a row
-// in slices of at most 4096, two runs to a thread, and the CTA's 256 threads
-// take 256 / TC rows at a time where a slice needs only TC of them. Each thread
+// is read once: a CTA of 256 or 512 threads takes rows of up to 4096 or 8192
+// columns, two runs to a thread (256 / TC rows at a time where a row needs only
+// TC of them); beyond, a cluster of CTAs takes a row in slices of 8192. Each thread
 // keeps the sums of dy * n of its 16 columns over all its rows; at the end they
 // are added over the CTA's row groups and written as one row of partial sums,
 // and a second kernel adds those rows in order (no atomics: the order never
 // changes).
 
-constexpr int kBwdThreads = 256;
+constexpr int kBwdMaxThreads = 512;
 constexpr int kBwdRuns = 2;          // runs to a thread, TC * 8 columns apart
-constexpr int kBwdMaxParts = 512;    // rows of partial sums at most
-constexpr int64_t kBwdMaxCols = int64_t{kMaxCluster} * kBwdThreads * kBwdRuns * kVec;
-template <bool BF16>
-constexpr int kBwdCtasPerSm = BF16 ? 3 : 2;
+constexpr int kBwdMaxParts = 640;    // rows of partial sums at most
+constexpr int64_t kBwdMaxCols = int64_t{kMaxCluster} * kBwdMaxThreads * kBwdRuns * kVec / 2;   // 65536
+template <int T, bool BF16>
+constexpr int kBwdCtasPerSm = (BF16 ? 1024 : 512) / T;
 
 struct NormBwdParams {
   const void* dy;
@@ -444,20 +437,21 @@ struct NormBwdParams {
   int weight_bf16;
 };
 
-template <bool BF16, bool SKIP>
-__global__ void __launch_bounds__(kBwdThreads, kBwdCtasPerSm<BF16>)
+template <int T, bool BF16, bool SKIP>
+__global__ void __launch_bounds__(T, kBwdCtasPerSm<T, BF16>)
     norm_backward_kernel(const __grid_constant__ NormBwdParams p) {
   constexpr int V = kBwdRuns;
-  constexpr int kWarps = kBwdThreads / 32;
+  constexpr int kWarps = T / 32;
   __shared__ float warp_sum[2][kWarps];
   __shared__ float cta_sum[2][kMaxCluster];   // a cluster's CTAs take one row at a time
-  __shared__ float2 dw_sum[V * 4][kBwdThreads];
+  extern __shared__ uint4 fetched[];          // [2][inputs][V][threads] runs: this row's and the next one's
+  float2 (&dw_sum)[V * 4][T] = *reinterpret_cast<float2 (*)[V * 4][T]>(fetched);   // at the end
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   const int rank = p.cluster > 1 ? static_cast<int>(bsg::cluster_ctarank()) : 0;
   const int part = blockIdx.x / p.cluster;
   const int tc = 1 << p.tc_log;
-  const int groups = kBwdThreads >> p.tc_log;
+  const int groups = T >> p.tc_log;
   const int group = tid >> p.tc_log;
   const int group_warps = tc / 32;
   const int run0 = (tid & (tc - 1)) * kVec;   // within the slice; run v is v * tc * 8 on
@@ -466,7 +460,6 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtasPerSm<BF16>)
 #pragma unroll
   for (int v = 0; v < V; ++v) in[v] = run0 + v * tc * kVec < p.slice && c0 + v * tc * kVec < p.cols;
 
-  bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
 
   float2 w[V][4], dw[V][4];
@@ -483,28 +476,49 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtasPerSm<BF16>)
   int64_t r = static_cast<int64_t>(part) * groups + group;
   int64_t e = r * p.cols + c0;
   const int64_t e_step = stride * p.cols;
-  int buf = 0;
-  for (int64_t base = static_cast<int64_t>(part) * groups; base < p.rows; base += stride) {
-    const bool exists = r < p.rows;
-    Run<BF16> dy[V], h[V], sk[SKIP ? V : 1];
-    float rs = 0.f;
+  // A thread's runs of the next row pass through places in shared memory that
+  // it alone reads (cp.async, two rows' worth), so that loads are in flight
+  // through this row's barrier and arithmetic.
+  constexpr int kRun = BF16 ? 16 : 32, kElem = BF16 ? 2 : 4, kInputs = SKIP ? 3 : 2;
+  const uint32_t own = bsg::smem_addr(fetched) + tid * kRun;
+  auto fetch = [&](int64_t row, int64_t at, int to) {
+    if (row < p.rows) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      dy[v] = h[v] = zero_run<BF16>();
-      if constexpr (SKIP) sk[v] = zero_run<BF16>();
-      if (in[v] && exists) {
-        dy[v] = load_run<BF16>(p.dy, e + v * tc * kVec);
-        h[v] = load_run<BF16>(p.h, e + v * tc * kVec);
-        if constexpr (SKIP) sk[v] = load_run<BF16>(p.skip, e + v * tc * kVec);
+      for (int v = 0; v < V; ++v) {
+        if (!in[v]) continue;
+        const int64_t o = (at + v * tc * kVec) * kElem;
+        const char* src[3] = {static_cast<const char*>(p.dy), static_cast<const char*>(p.h),
+                              static_cast<const char*>(p.skip)};
+#pragma unroll
+        for (int k = 0; k < kInputs; ++k)
+          fetch_run<BF16, true>(own + ((to * kInputs + k) * V + v) * (T * kRun), src[k] + o, true);
       }
     }
-    if (exists) rs = __ldg(p.rstd + r);
+    fetch_commit();
+  };
+  auto fetched_run = [&](int from, int input, int v) {
+    Run<BF16> x;
+    const uint4* at = fetched + (((from * kInputs + input) * V + v) * T + tid) * (kRun / 16);
+#pragma unroll
+    for (int k = 0; k < (BF16 ? 1 : 2); ++k) x.w[k] = at[k];
+    return x;
+  };
+  int buf = 0;
+  fetch(r, e, 0);
+  float rs_next = r < p.rows ? __ldg(p.rstd + r) : 0.f;
+  for (int64_t base = static_cast<int64_t>(part) * groups; base < p.rows; base += stride) {
+    const bool exists = r < p.rows;
+    fetch(r + stride, e + e_step, buf ^ 1);
+    const float rs = rs_next;
+    rs_next = r + stride < p.rows ? __ldg(p.rstd + r + stride) : 0.f;
+    fetch_wait<1>();
     float2 s2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      if (!in[v] || !exists) continue;
       float2 a[4], b[4];
-      widen<BF16>(dy[v], a);
-      widen<BF16>(h[v], b);
+      widen<BF16>(fetched_run(buf, 0, v), a);
+      widen<BF16>(fetched_run(buf, 1, v), b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 n = mul2(b[i], both(rs));
@@ -531,22 +545,24 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtasPerSm<BF16>)
       }
     }
     const float m = s * inv_cols;   // mean(dn * n)
+    // (the runs are read again rather than held in registers past the barrier)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      if (!in[v] || !exists) continue;
       float2 a[4], b[4];
-      widen<BF16>(dy[v], a);
-      widen<BF16>(h[v], b);
+      widen<BF16>(fetched_run(buf, 0, v), a);
+      widen<BF16>(fetched_run(buf, 1, v), b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 n = mul2(b[i], both(rs));
         a[i] = mul2(bsg::ffma2(n, both(-m), mul2(a[i], w[v][i])), both(rs));
       }
       if constexpr (SKIP) {
-        widen<BF16>(sk[v], b);
+        widen<BF16>(fetched_run(buf, 2, v), b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = add2(a[i], b[i]);
       }
-      if (in[v] && exists) store_run<BF16>(p.dx, e + v * tc * kVec, narrow<BF16>(a));
+      store_run<BF16>(p.dx, e + v * tc * kVec, narrow<BF16>(a));
     }
     r += stride;
     e += e_step;
@@ -555,7 +571,13 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtasPerSm<BF16>)
     buf ^= 1;
   }
 
-  // the row groups' sums, added in order by the first group's threads
+  // The next kernel may start now, not before: this one fills every SM, and a
+  // kernel that settled beside its last CTAs to come would keep them waiting
+  // (61 against 51 us on 8192 x 4096 BF16).
+  bsg::grid_launch_dependents();
+  // the row groups' sums, added in order by the first group's threads (in the
+  // fetched runs' place: none is in flight, and all have been read)
+  __syncthreads();
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -579,7 +601,6 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int
   __shared__ float sums[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
   float s = 0.f;
   if (c < cols) {
@@ -601,8 +622,9 @@ int64_t bwd_parts_bound(int64_t rows) { return rows < kBwdMaxParts ? rows : kBwd
 }  // namespace bsgn
 
 namespace bsgr {
-bsgemm_status launch_column_sum(const float* part, int parts, int64_t cols, float* out, cudaStream_t stream) {
-  return launch_rows(bsgn::column_sum_kernel, (cols + 31) / 32, 1024, 0, 1, stream, part, parts, cols, out);
+bsgemm_status launch_column_sum(const float* part, int parts, int64_t cols, float* out, cudaStream_t stream,
+                                const bsg_host::DeviceInfo& dev) {
+  return launch_rows<bsgn::column_sum_kernel>(dev, (cols + 31) / 32, 1024, 0, 1, stream, part, parts, cols, out);
 }
 }  // namespace bsgr
 
@@ -700,15 +722,17 @@ extern "C" bsgemm_status bsgemm_rms_norm_backward(int src_dtype, int weight_dtyp
   p.rows = rows;
   p.cols = cols;
   p.weight_bf16 = weight_dtype == BSGEMM_SRC_BF16;
+  const int64_t span = bsgn::kBwdRuns * bsgr::kVec;   // columns to a thread
+  const int threads = cols <= 256 * span ? 256 : 512;
   p.cluster = 1;
-  while (int64_t{p.cluster} * bsgn::kBwdThreads * bsgn::kBwdRuns * bsgr::kVec < cols) p.cluster *= 2;
+  while (int64_t{p.cluster} * threads * span < cols) p.cluster *= 2;
   const int64_t runs = cols / bsgr::kVec;
   p.slice = static_cast<int>((runs + p.cluster - 1) / p.cluster * bsgr::kVec);
   p.tc_log = 5;
-  while ((bsgn::kBwdRuns * bsgr::kVec << p.tc_log) < p.slice) ++p.tc_log;
-  const int64_t batch = bsgn::kBwdThreads >> p.tc_log;
+  while ((span << p.tc_log) < p.slice) ++p.tc_log;
+  const int64_t batch = threads >> p.tc_log;
   const int64_t batches = (rows + batch - 1) / batch;
-  int64_t parts = int64_t{dev.num_sms} * (bf16 ? bsgn::kBwdCtasPerSm<true> : bsgn::kBwdCtasPerSm<false>) / p.cluster;
+  int64_t parts = int64_t{dev.num_sms} * ((bf16 ? 1024 : 512) / threads) / p.cluster;
   if (parts < 1) parts = 1;
   if (parts > batches) parts = batches;
   if (parts > bsgn::kBwdMaxParts) parts = bsgn::kBwdMaxParts;
@@ -717,15 +741,17 @@ extern "C" bsgemm_status bsgemm_rms_norm_backward(int src_dtype, int weight_dtyp
   p.part = parts == 1 ? dweight : static_cast<float*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t grid = parts * p.cluster;
-  auto go = [&](auto kern) -> bsgemm_status {
-    if (p.cluster > 8) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return BSGEMM_ERR_CUDA;
-    }
-    return bsgr::launch_rows(kern, grid, bsgn::kBwdThreads, 0, p.cluster, s, p);
-  };
-  if (bf16) st = skip ? go(bsgn::norm_backward_kernel<true, true>) : go(bsgn::norm_backward_kernel<true, false>);
-  else      st = skip ? go(bsgn::norm_backward_kernel<false, true>) : go(bsgn::norm_backward_kernel<false, false>);
+#define BSGN_GO(T, BF, SK)                                                                                    \
+  bsgr::launch_rows<bsgn::norm_backward_kernel<T, BF, SK>>(                                                   \
+      dev, grid, T, 2 * (SK ? 3 : 2) * bsgn::kBwdRuns * T * (BF ? 16 : 32), p.cluster, s, p)
+  if (threads == 256) {
+    if (bf16) st = skip ? BSGN_GO(256, true, true) : BSGN_GO(256, true, false);
+    else      st = skip ? BSGN_GO(256, false, true) : BSGN_GO(256, false, false);
+  } else {
+    if (bf16) st = skip ? BSGN_GO(512, true, true) : BSGN_GO(512, true, false);
+    else      st = skip ? BSGN_GO(512, false, true) : BSGN_GO(512, false, false);
+  }
+#undef BSGN_GO
   if (st != BSGEMM_OK || parts == 1) return st;
-  return bsgr::launch_column_sum(p.part, p.parts, cols, dweight, s);
+  return bsgr::launch_column_sum(p.part, p.parts, cols, dweight, s, dev);
 }

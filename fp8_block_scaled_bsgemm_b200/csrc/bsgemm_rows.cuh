@@ -13,6 +13,7 @@
 #include <cstdint>
 
 #include "bsgemm.h"
+#include "bsgemm_host.h"
 #include "ptx.cuh"
 
 namespace bsgr {
@@ -213,7 +214,7 @@ inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintp
 // Sizes, types and device of a row-wise call; nothing is launched on an error.
 inline bsgemm_status check_rows(int src_dtype, int64_t rows, int64_t cols) {
   if (src_dtype != BSGEMM_SRC_F32 && src_dtype != BSGEMM_SRC_BF16) return BSGEMM_ERR_INVALID_ARG;
-  if (rows <= 0 || cols <= 0 || rows > (1 << 30) || cols > (1 << 30)) return BSGEMM_ERR_INVALID_ARG;
+  if (rows <= 0 || cols <= 0 || rows > (1 << 30) || cols > (1 << 24)) return BSGEMM_ERR_INVALID_ARG;
   return cols % 16 ? BSGEMM_ERR_MISALIGNED : BSGEMM_OK;
 }
 
@@ -245,14 +246,25 @@ inline size_t blocks_bytes(int64_t rows, int64_t cols, int g) {
 }
 
 // Adds up `parts` rows of partial sums in order: out[c] = sum_i part[i][c].
-bsgemm_status launch_column_sum(const float* part, int parts, int64_t cols, float* out, cudaStream_t stream);
+bsgemm_status launch_column_sum(const float* part, int parts, int64_t cols, float* out, cudaStream_t stream,
+                                const bsg_host::DeviceInfo& dev);
 
-// A launch that may overlap its set-up with the end of the stream's previous
-// kernel (every kernel here waits for it before touching global memory).
-template <typename... A, typename... B>
-bsgemm_status launch_rows(void (*kern)(A...), int64_t grid, int threads, size_t smem, int cluster,
-                          cudaStream_t stream, B... args) {
+// Launches Kern with `smem` bytes of dynamic shared memory (the same in every
+// call of a kernel).
+// Its set-up may overlap the end of the stream's previous kernel (every kernel
+// here waits for it before touching global memory).
+template <auto Kern, typename... A>
+bsgemm_status launch_rows(const bsg_host::DeviceInfo& dev, int64_t grid, int threads, int smem, int cluster,
+                          cudaStream_t stream, A... args) {
   if (grid < 1 || grid > 0x7FFFFFFFll) return BSGEMM_ERR_INVALID_ARG;
+  static bsg_host::PerDeviceOnce setup;
+  if (!setup.done(dev.ordinal)) {
+    if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        // clusters of 16 are beyond the portable size
+        cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return BSGEMM_ERR_CUDA;
+    setup.mark(dev.ordinal);
+  }
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -267,7 +279,7 @@ bsgemm_status launch_rows(void (*kern)(A...), int64_t grid, int threads, size_t 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, Kern, args...) != cudaSuccess) {
     (void)cudaGetLastError();
     return BSGEMM_ERR_CUDA;
   }

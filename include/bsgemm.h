@@ -276,8 +276,8 @@ bsgemm_status bsgemm_fp8_gemm_residual(int layout, int a_format, int b_format, c
 /* ---- norm, activation and their gradients ---------------------------------
  * The steps between two GEMMs of a transformer sublayer, each fused with the
  * quantisation of its result into the next GEMM's operand. Shared rules:
- *   - matrices are dense row-major [rows, cols], rows, cols in 1 .. 2^30,
- *     cols % 16 == 0 (else BSGEMM_ERR_MISALIGNED), of src_dtype (FP32 or BF16;
+ *   - matrices are dense row-major [rows, cols], rows in 1 .. 2^30, cols in
+ *     1 .. 2^24 (else BSGEMM_ERR_INVALID_ARG), cols % 16 == 0 (else BSGEMM_ERR_MISALIGNED), of src_dtype (FP32 or BF16;
  *     one type for all of a call's matrices), device pointers 16-byte aligned;
  *   - q, scales, gran and fp8_format are the quantiser's (above), except that
  *     a block whose amax / FMAX rounds to 0 also gets scale 1. Values are

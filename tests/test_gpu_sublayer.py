@@ -110,8 +110,8 @@ def test_norm_non_finite_rows_spoil_no_other_row():
 
 def bwd_depth(rows, cols):
     """Additions in a row: 8 in a run, 5 in the warp, up to 16 warps and 16 CTAs. In a column: a part's
-    rows (each an addition), up to 16 row groups, up to 512 parts."""
-    return 8 + 5 + 16 + 16, rows + 16 + 512
+    rows (each an addition), up to 16 row groups, up to 640 parts."""
+    return 8 + 5 + 16 + 16, rows + 16 + 640
 
 
 def check_norm_backward(dy, h, w, rstd, skip, dx, dw):

@@ -44,7 +44,7 @@ def _norm(L, x=MB, residual=2 * MB, weight=3 * MB, eps=1e-6, rows=64, cols=64, g
     (dict(residual=None), INVALID), (dict(h=None), INVALID),             # both or neither
     (dict(src=2), INVALID), (dict(wdt=-1), INVALID), (dict(fmt=2), INVALID),
     (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
-    (dict(rows=0), INVALID), (dict(cols=0), INVALID), (dict(rows=-3), INVALID), (dict(rows=(1 << 30) + 1), INVALID), (dict(rstd=None), INVALID),
+    (dict(rows=0), INVALID), (dict(cols=0), INVALID), (dict(rows=-3), INVALID), (dict(rows=(1 << 30) + 1), INVALID), (dict(cols=(1 << 24) + 16), INVALID), (dict(rstd=None), INVALID),
     (dict(gran=32), GRAN), (dict(cols=72), MISALIGNED), (dict(x=MB + 8), MISALIGNED), (dict(weight=3 * MB + 4), MISALIGNED),
     (dict(q=5 * MB + 8), MISALIGNED), (dict(scales=6 * MB + 2), MISALIGNED), (dict(rstd=7 * MB + 1), MISALIGNED),
     (dict(h=MB + 16), INVALID), (dict(h=2 * MB - 16), INVALID),          # a shifted part of an input
@@ -109,7 +109,7 @@ def test_activation_backward_refusals(change, want):
 def test_workspace_sizes():
     L = bsg.lib()
     assert L.bsgemm_rms_norm_backward_workspace(1, 64) == 64 * 4
-    assert L.bsgemm_rms_norm_backward_workspace(1 << 20, 4096) == 512 * 4096 * 4
+    assert L.bsgemm_rms_norm_backward_workspace(1 << 20, 4096) == 640 * 4096 * 4
     assert L.bsgemm_rms_norm_backward_workspace(0, 64) == 0
     assert L.bsgemm_activation_backward_workspace(128, 64, 128) == 0      # one row of sums is dbias itself
     assert L.bsgemm_activation_backward_workspace(129, 64, 128) == 2 * 64 * 4
