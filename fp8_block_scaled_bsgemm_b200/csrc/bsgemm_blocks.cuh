@@ -15,6 +15,8 @@
 // its rows each. A thread computes its values once, keeps them in registers
 // past the block's amax, and encodes them.
 #pragma once
+#include <atomic>
+
 #include "bsgemm_host.h"
 #include "bsgemm_rows.cuh"
 
@@ -276,7 +278,27 @@ bsgemm_status launch_blocks(BlockParams& p, const Op& op, cudaStream_t stream, c
   constexpr int kSmem = kBufBytes<G, BF16, IN2> * kBufs<G, BF16, IN2>;
   p.row_blocks = static_cast<int>((p.rows + G - 1) / G);
   p.col_blocks = static_cast<int>((p.cols + G - 1) / G);
-  int64_t units = int64_t{dev.num_sms} * kCtasPerSm<G> / kParts<G>;   // blocks taken at the same time
+  // Blocks taken at the same time: no more clusters than can be resident, since
+  // the rest would begin when the others have ended (a GPC's SMs do not hold a
+  // whole number of clusters: 74 of them for 148 SMs doubled the time).
+  int64_t units = int64_t{dev.num_sms} * kCtasPerSm<G>;
+  if constexpr (kParts<G> > 1) {
+    static std::atomic<int> resident[64];
+    const int slot = dev.ordinal >= 0 && dev.ordinal < 64 ? dev.ordinal : -1;
+    int n = slot >= 0 ? resident[slot].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+      constexpr auto kern = block_quant_kernel<G, BF16, FMT, Op>;
+      if (!prepare_rows<block_quant_kernel<G, BF16, FMT, Op>>(dev, kSmem)) return BSGEMM_ERR_CUDA;
+      RowsLaunch l(units, kThreads<G>, kSmem, kParts<G>, stream);
+      l.cfg.numAttrs = 1;   // the cluster shape alone decides residency
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &l.cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return BSGEMM_ERR_CUDA;
+      }
+      if (slot >= 0) resident[slot].store(n, std::memory_order_relaxed);
+    }
+    units = n;
+  }
   const int64_t blocks = static_cast<int64_t>(p.row_blocks) * p.col_blocks;
   if (units > blocks) units = blocks;
   p.step_rb = static_cast<int>(units / p.col_blocks);

@@ -249,36 +249,48 @@ inline size_t blocks_bytes(int64_t rows, int64_t cols, int g) {
 bsgemm_status launch_column_sum(const float* part, int parts, int64_t cols, float* out, cudaStream_t stream,
                                 const bsg_host::DeviceInfo& dev);
 
-// Launches Kern with `smem` bytes of dynamic shared memory (the same in every
-// call of a kernel).
-// Its set-up may overlap the end of the stream's previous kernel (every kernel
-// here waits for it before touching global memory).
+// Once per device, before Kern's first launch with `smem` bytes of dynamic
+// shared memory (the same in every call of a kernel).
+template <auto Kern>
+bool prepare_rows(const bsg_host::DeviceInfo& dev, int smem) {
+  static bsg_host::PerDeviceOnce setup;
+  if (setup.done(dev.ordinal)) return true;
+  if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      // clusters of 16 are beyond the portable size
+      cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return false;
+  setup.mark(dev.ordinal);
+  return true;
+}
+
+struct RowsLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  RowsLaunch(int64_t grid, int threads, int smem, int cluster, cudaStream_t stream) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    // the kernel's set-up may overlap the end of the stream's previous kernel
+    // (every kernel here waits for it before touching global memory)
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = cluster > 1 ? attr : attr + 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+  }
+};
+
 template <auto Kern, typename... A>
 bsgemm_status launch_rows(const bsg_host::DeviceInfo& dev, int64_t grid, int threads, int smem, int cluster,
                           cudaStream_t stream, A... args) {
   if (grid < 1 || grid > 0x7FFFFFFFll) return BSGEMM_ERR_INVALID_ARG;
-  static bsg_host::PerDeviceOnce setup;
-  if (!setup.done(dev.ordinal)) {
-    if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        // clusters of 16 are beyond the portable size
-        cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-      return BSGEMM_ERR_CUDA;
-    setup.mark(dev.ordinal);
-  }
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (!prepare_rows<Kern>(dev, smem)) return BSGEMM_ERR_CUDA;
+  RowsLaunch l(grid, threads, smem, cluster, stream);
+  const cudaLaunchConfig_t& cfg = l.cfg;
   if (cudaLaunchKernelEx(&cfg, Kern, args...) != cudaSuccess) {
     (void)cudaGetLastError();
     return BSGEMM_ERR_CUDA;
