@@ -567,10 +567,14 @@ struct ResidualChunks {
   static constexpr int kCols = F32 ? 32 : 64;   // columns per chunk
   static constexpr int kChunks = 2 * NP / kCols;
 
-  // the previous store must have finished reading the buffer, and every lane
-  // the chunk before this one
+  // The previous store must have finished reading the buffer, and every lane
+  // the chunk before this one: each lane's fence holds its reads (and stores)
+  // before the asynchronous write into the same places. Without it some of the
+  // reads came after the next chunk's arrival.
   static __device__ __forceinline__ void start(const CUtensorMap* tm, uint32_t buf, uint32_t bar, int m0, int n0, int c,
                                                uint32_t lane) {
+    fence_proxy_async_smem();
+    __syncwarp();
     if (lane == 0) {
       bulk_wait_group_read0();
       mbar_arrive_expect_tx(bar, kEpiChunkBytes);
@@ -667,10 +671,7 @@ struct ResidualChunks {
     uint4 v[8];
     take(buf, lane, v);
     apply_epi_staged<NP, true>(p, buf, n0, acc, lane);
-    if constexpr (kChunks > 1) {
-      fence_proxy_async_smem();   // the bias's stores come before the load into the same buffer
-      start(tm, buf, bar, m0, n0, s.started++, lane);
-    }
+    if constexpr (kChunks > 1) start(tm, buf, bar, m0, n0, s.started++, lane);
     add(s.added++, v, acc);
 #pragma unroll 1
     while (s.added < kChunks)

@@ -17,7 +17,6 @@
 // All of it is memory-bound: 2-byte streams of 3 reads or writes per element
 // and a byte of codes forward, 4 backward.
 #include <cmath>
-#include <type_traits>
 
 #include "bsgemm_blocks.cuh"
 
@@ -191,7 +190,7 @@ struct Scaled {
   __device__ __forceinline__ Rows<NP> rows(int64_t row, int left, int step) const {
     Rows<NP> r;
 #pragma unroll
-    for (int j = 0; j < NP; ++j) r.rs[j] = j * step < left ? __ldg(rstd + row + j * step) : 0.f;
+    for (int j = 0; j < NP; ++j) r.rs[j] = j * step < left ? __ldcg(rstd + row + j * step) : 0.f;
     return r;
   }
   __device__ __forceinline__ Cols cols(int col, bool exists) const {
@@ -251,6 +250,8 @@ __global__ void __launch_bounds__(kFewThreads) norm_few_kernel(const __grid_cons
   // ---- pass 1: h and its squares
   Run<BF16> h[K], keep[K];
   float2 ss = both(0.f);
+#pragma unroll
+  for (int k = 0; k < K; ++k) keep[k] = zero_run<BF16>();
   for (int b0 = rank + p.cluster * slot; b0 < p.col_blocks; b0 += K * step) {
     Run<BF16> res[RES ? K : 1];
 #pragma unroll
@@ -505,12 +506,12 @@ __global__ void __launch_bounds__(T, kBwdCtasPerSm<T, BF16>)
   };
   int buf = 0;
   fetch(r, e, 0);
-  float rs_next = r < p.rows ? __ldg(p.rstd + r) : 0.f;
+  float rs_next = r < p.rows ? __ldcg(p.rstd + r) : 0.f;
   for (int64_t base = static_cast<int64_t>(part) * groups; base < p.rows; base += stride) {
     const bool exists = r < p.rows;
     fetch(r + stride, e + e_step, buf ^ 1);
     const float rs = rs_next;
-    rs_next = r + stride < p.rows ? __ldg(p.rstd + r + stride) : 0.f;
+    rs_next = r + stride < p.rows ? __ldcg(p.rstd + r + stride) : 0.f;
     fetch_wait<1>();
     float2 s2 = both(0.f);
 #pragma unroll
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(T, kBwdCtasPerSm<T, BF16>)
       s = warp_sum[buf][(warp & ~(group_warps - 1)) + (lane & (group_warps - 1))];
       for (int o = group_warps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (p.cluster > 1) {
-        // (slices of a cluster have more than 2048 columns: one row group)
+        // (slices of a cluster have more than 4096 columns: one row group)
         if (tid < p.cluster) st_cluster_f32(bsg::mapa_shared(bsg::smem_addr(&cta_sum[buf][rank]), tid), s);
         __syncwarp();
         bsg::cluster_sync_all();

@@ -284,9 +284,10 @@ bsgemm_status bsgemm_fp8_gemm_residual(int layout, int a_format, int b_format, c
  *     quantised as computed in FP32, without a rounding to src_dtype between;
  *   - sums, statistics and gradients of vectors are FP32, added in a fixed
  *     order: the same inputs give bit-identical outputs;
- *   - inputs must be finite. A NaN or infinity spoils the codes of its row
- *     (norm) or of itself (activation) and may make its blocks' scales and
- *     the sums over it infinite or NaN; nothing else is affected;
+ *   - inputs must be finite. With a NaN or infinity the codes of its row
+ *     (norm, and its gradient's dx) or of itself (activation), the scales of
+ *     those blocks and the sums over it are unspecified; nothing else is
+ *     affected, and the call completes;
  *   - errors are found before any launch; nothing is written then. Unknown
  *     types, formats or activations, NULL where a pointer is needed:
  *     BSGEMM_ERR_INVALID_ARG. gran: BSGEMM_ERR_UNSUPPORTED_GRAN;

@@ -1,4 +1,8 @@
 """The operators around the GEMM on a B200, against plain 64-bit forms (tests/sublayer_util.py)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -302,6 +306,37 @@ def test_gemm_residual(gran, out_dtype, tuning, M, N, K, layout):
     assert bsg.get_last_device_status() == 0
 
 
+@pytest.mark.parametrize("M,N,K,gran,tuning", [
+    (4096, 4096, 4096, 128, None), (2048, 4096, 14336, 128, None), (4096, 4096, 2064, 64, None), (4096, 4096, 4096, 256, None),
+    (4096, 4096, 2064, 128, {"variant": "cta_pair"}), (4096, 4096, 4096, 64, {"variant": "data_parallel", "bnq": 256, "stream_k": -1}),
+    (4096, 4096, 1040, 128, {"variant": "data_parallel", "bnq": 128, "stream_k": -1}),
+    (4096, 4096, 400, 128, None), (4096, 2064, 144, 64, None)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_gemm_residual_on_many_tiles(M, N, K, gran, tuning, out_dtype):
+    """Persistent CTAs walk several tiles, each with its residual on its way in the last K-blocks: every element, four
+    times over, against the FP32 product without a residual.
+
+    The two sum the same block products; the residual joins some K-blocks before the end, so the additions after it,
+    kGap * kChunks <= 12 of them and the bias's, round a sum that holds it: 14 U (|residual| + sum |a b|), and the
+    output's own rounding. The plain product's additions may be ordered otherwise (stream-K): K / 64 U sum |a b|.
+    """
+    gen = gen_of(17, M, K)
+    a, b, sa, sb, A, B = gemm_inputs(gen, M, N, K, "nt", gran)
+    mag = A.float().abs() @ B.float().abs().t()
+    del A, B
+    bias = randn(gen, N)
+    base = bsg.gemm(a, b, sa, sb, gran=gran, out_dtype=torch.float32).double()
+    for k in range(4):
+        residual = randn(gen, M, N, dtype=out_dtype, scale=20.0)
+        kw = dict(bias=bias) if k & 1 else {}
+        out = bsg.gemm(a, b, sa, sb, gran=gran, tuning=tuning, out_dtype=out_dtype, residual=residual, **kw)
+        want = base + residual.double() + (bias.double() if kw else 0)
+        tol = (14 * (residual.double().abs() + mag) + K / 64 * mag + (bias.abs() if kw else 0)) * su.U
+        tol = tol + (want.abs() + tol) * su.out_rounding(out_dtype)
+        bad = (out.double() - want).abs() > tol
+        assert not bad.any(), (k, int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
 def test_gemm_residual_leaves_what_lies_behind_the_output():
     gen = gen_of(8)
     a, b, sa, sb, A, B = gemm_inputs(gen, 130, 264, 272, "nt", 128)
@@ -458,6 +493,111 @@ def test_both_marshallings_agree(monkeypatch):
     assert fast.act(x, 0, 128, 0) == 1 and fast.act_backward(x, x, 0, 128, 0, True) is None
     assert fast.norm_backward(x, x, w, w.double(), None) is None
     assert fast.gemm(0, 128, x, x, w, w, None, 0, False, None) is None
+
+
+FRESH_CAPTURE = """
+import torch
+import fp8_block_scaled_bsgemm_b200 as bsg
+x = torch.randn(300, 528, device="cuda").bfloat16()
+w = torch.ones(528, device="cuda")
+rstd = torch.ones(300, device="cuda")
+g = torch.cuda.CUDAGraph()
+s = torch.cuda.Stream()
+s.wait_stream(torch.cuda.current_stream())
+with torch.cuda.graph(g, stream=s):
+    outs = []
+    for gran in (64, 256):
+        outs += bsg.rms_norm_quantize(x, w, residual=x, gran=gran, return_rstd=True)
+        outs += bsg.rms_norm_quantize(x[:3], w, gran=gran, return_rstd=True)[:2]
+        outs += bsg.activation_quantize(x, "gelu", gran=gran)
+        outs += bsg.activation_backward_quantize(x, x, "relu", gran=gran)
+    outs += bsg.rms_norm_backward(x, x, w, rstd)
+g.replay()
+torch.cuda.synchronize()
+got = [o.clone() for o in outs]
+want = []
+for gran in (64, 256):
+    want += bsg.rms_norm_quantize(x, w, residual=x, gran=gran, return_rstd=True)
+    want += bsg.rms_norm_quantize(x[:3], w, gran=gran, return_rstd=True)[:2]
+    want += bsg.activation_quantize(x, "gelu", gran=gran)
+    want += bsg.activation_backward_quantize(x, x, "relu", gran=gran)
+want += bsg.rms_norm_backward(x, x, w, rstd)
+assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+print("ok")
+"""
+
+
+def test_the_first_call_of_a_process_can_be_a_captured_one():
+    """No call before the capture: set-up of the kernels happens inside it."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FRESH_CAPTURE], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements: the last rows as if they stood alone, and the sums over all rows."""
+    rows, cols, g = 131_200, 32_768, 128
+    assert rows * cols > 1 << 32
+    gen = gen_of(16)
+    bf = torch.bfloat16
+    block = randn(gen, g, cols, dtype=bf)            # every row block the same, but for the last one
+    tail = randn(gen, g, cols, dtype=bf)
+    x = block.repeat(rows // g, 1)
+    x[-g:] = tail
+    w = randn(gen, cols)
+    want = bsg.rms_norm_quantize(tail, w, residual=tail, return_rstd=True)
+    q, s, h, rstd = bsg.rms_norm_quantize(x, w, residual=x, residual_out=x, return_rstd=True)
+    assert h is x
+    for got, alone in ((q, want[0]), (s, want[1]), (x, want[2]), (rstd, want[3])):
+        n = alone.shape[0]
+        # a row alone is summed by more threads: rstd may differ in its last places, and codes next to a border with it
+        if got is x:
+            assert torch.equal(got[-n:], alone)
+        else:
+            a, b = got[-n:].view(torch.uint8).float(), alone.view(torch.uint8).float()
+            assert ((a != b).float().mean() < 1e-3) if got is q else torch.allclose(got[-n:], alone, rtol=1e-5)
+    del q, s
+    dy = x.clone()
+    dx, dw = bsg.rms_norm_backward(dy, x, w, rstd, dx=dy)
+    assert dx is dy
+    check_norm_backward(want[2], want[2], w, rstd[-g:], None, dx[-g:],
+                        su.norm_backward(want[2], want[2], w, rstd[-g:])[1].float())
+    head = su.norm_backward(su.stream(block, block), su.stream(block, block), w, rstd[:g])[1]
+    last = su.norm_backward(want[2], want[2], w, rstd[-g:])[1]
+    total = head * (rows // g - 1) + last
+    n = su.stream(block, block).double()
+    mag = (n * n * rstd[:g].double()[:, None]).abs().sum(0) * (rows // g)
+    assert ((dw.double() - total).abs() <= mag * (rows / 100 + 700) * su.U).all()
+    del dx, dy, x, h
+    torch.cuda.empty_cache()
+    z = block.repeat(rows // g, 1)
+    z[-g:] = tail
+    q, s = bsg.activation_quantize(z, "gelu")
+    alone = bsg.activation_quantize(tail, "gelu")
+    assert torch.equal(q[-g:], alone[0]) and torch.equal(s[-1:], alone[1])
+    del q, s
+    q, s, db = bsg.activation_backward_quantize(z, z, "relu")
+    alone = bsg.activation_backward_quantize(tail, tail, "relu")
+    assert torch.equal(q[-g:], alone[0]) and torch.equal(s[-1:], alone[1])
+    sums = block.double().clamp(min=0).sum(0) * (rows // g - 1) + tail.double().clamp(min=0).sum(0)
+    assert ((db.double() - sums).abs() <= sums * (g + rows // g) * su.U).all()
+
+
+def test_scales_are_correctly_rounded_quotients():
+    """amax / FMAX by the corrected product: bit for bit the division, over a binade and a range of exponents."""
+    for fmt in ("e4m3", "e5m2"):
+        mant = torch.arange(1 << 18, device="cuda", dtype=torch.int64) * 32 + 7
+        for exponent in (-100, -40, 0, 40, 100, 126):
+            v = torch.ldexp(1.0 + mant.double() / (1 << 23), torch.tensor(exponent, device="cuda")).float()
+            x = torch.zeros(v.numel(), 16, device="cuda")
+            x[:, 3] = v
+            x = x.view(1, -1)                      # one row: a block is 64 columns, 4 values
+            q, s, _ = bsg.activation_backward_quantize(x.view(-1, 1 << 16), None, gran=64, fmt=fmt, bias_grad=False)
+            # (divided on the CPU: torch's CUDA kernel multiplies by the reciprocal of a scalar divisor)
+            want = (su.block_amax(x.view(-1, 1 << 16), 64).cpu() / su.FMAX[fmt]).cuda()
+            assert want.dtype == torch.float32
+            want = torch.where(want > 0, want, torch.ones_like(want))
+            assert torch.equal(s, want)
 
 
 # ------------------------------------------------------------------ a sublayer
