@@ -103,7 +103,9 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
   extern __shared__ uint4 fetched[];   // [kBuf][inputs][NP][T] runs
   __shared__ float warp_max[2][W];
   __shared__ float part_max[2][P];
-  __shared__ float col_sum[SUMS ? 2 : 1][SUMS ? W : 1][SUMS ? G : 1];
+  // column sums of each group of L threads; a run's first four columns lie in
+  // the first half of a row, its others in the second (no bank conflicts)
+  __shared__ float4 col_sum[SUMS ? 2 : 1][SUMS ? RP : 1][2][SUMS ? L : 1];
 
   constexpr int kElem = BF16 ? 2 : 4;
   const int tid = threadIdx.x;
@@ -213,19 +215,15 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
     if ((tid & 31) == 0) warp_max[par][tid / 32] = amax;
     if constexpr (SUMS) {
       if (p.part != nullptr) {
-        // the thread's rows, then the warp's (32 / L of them hold the same columns)
+        float2 s[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float2 s = v[0][i];
+          s[i] = v[0][i];
 #pragma unroll
-          for (int j = 1; j < NP; ++j) s = add2(s, v[j][i]);
-#pragma unroll
-          for (int o = L; o < 32; o *= 2) {
-            s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-            s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-          }
-          if ((tid & 31) < L) *reinterpret_cast<float2*>(&col_sum[par][tid / 32][col8 + 2 * i]) = s;
+          for (int j = 1; j < NP; ++j) s[i] = add2(s[i], v[j][i]);
         }
+        col_sum[par][tid / L][0][tid % L] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+        col_sum[par][tid / L][1][tid % L] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
       }
     }
     // (a copy of the exchanged values is written again two blocks on, past a
@@ -260,9 +258,10 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
     }
     if constexpr (SUMS) {
       if (p.part != nullptr && tid < G && c0 + tid < cols) {
-        float sum = col_sum[par][0][tid];
+        const float* of = reinterpret_cast<const float*>(&col_sum[par][0][(tid >> 2) & 1][tid >> 3]) + (tid & 3);
+        float sum = of[0];
 #pragma unroll
-        for (int k = 1; k < W; ++k) sum += col_sum[par][k][tid];
+        for (int k = 1; k < RP; ++k) sum += of[k * G];
         p.part[part_row * p.cols + c0 + tid] = sum;
       }
     }
