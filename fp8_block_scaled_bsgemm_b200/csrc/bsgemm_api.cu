@@ -12,6 +12,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "bsgemm.h"
 #include "bsgemm_host.h"
@@ -87,6 +88,13 @@ std::map<int, DeviceInfo> g_dev;
 // for the (device, handle).
 std::map<std::pair<int, unsigned long long>, Workspace> g_ws;
 std::map<std::pair<int, uintptr_t>, unsigned long long> g_ids;
+// Buffers that a graph may still use, outgrown by later calls.
+struct Outgrown {
+  int dev;
+  void* p;
+  size_t n_counters;   // 0: partial tiles
+};
+std::vector<Outgrown> g_outgrown;
 
 bsgemm_status device_info(DeviceInfo& out) {
   int dev = 0;
@@ -144,7 +152,8 @@ bsgemm_status get_workspace(cudaStream_t stream, size_t ws_bytes, size_t n_count
     if (capturing) return BSGEMM_ERR_CUDA;
   }
   if (w.ws_bytes < ws_bytes) {
-    if (w.ws && cudaFreeAsync(w.ws, stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
+    if (w.ws && w.in_graph) g_outgrown.push_back({dev, w.ws, 0});
+    else if (w.ws && cudaFreeAsync(w.ws, stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
     w.ws = nullptr;
     w.ws_bytes = 0;
     size_t want = ws_bytes + ws_bytes / 4;
@@ -154,7 +163,8 @@ bsgemm_status get_workspace(cudaStream_t stream, size_t ws_bytes, size_t n_count
     w.ws_bytes = want;
   }
   if (w.n_counters < n_counters) {
-    if (w.counters && cudaFreeAsync(w.counters, stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
+    if (w.counters && w.in_graph) g_outgrown.push_back({dev, w.counters, w.n_counters});
+    else if (w.counters && cudaFreeAsync(w.counters, stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
     w.counters = nullptr;
     w.n_counters = 0;
     size_t want = n_counters < 1024 ? 1024 : n_counters * 2;
@@ -164,6 +174,7 @@ bsgemm_status get_workspace(cudaStream_t stream, size_t ws_bytes, size_t n_count
     if (cudaMemsetAsync(w.counters, 0, want * sizeof(int), stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
     w.n_counters = want;
   }
+  if (capturing) w.in_graph = true;
   out = w;
   return BSGEMM_OK;
 }
@@ -615,6 +626,8 @@ extern "C" bsgemm_status bsgemm_get_last_device_status(bsgemm_stream_t stream) {
     for (auto& kv : bsg_host::g_ws)
       if (kv.first.first == cur && kv.second.counters)
         cudaMemset(kv.second.counters, 0, kv.second.n_counters * sizeof(int));
+    for (const auto& o : bsg_host::g_outgrown)
+      if (o.dev == cur && o.n_counters) cudaMemset(o.p, 0, o.n_counters * sizeof(int));
   }
   if (cudaDeviceSynchronize() != cudaSuccess) return BSGEMM_ERR_CUDA;
   return static_cast<bsgemm_status>(v & 0xFF);
@@ -635,6 +648,14 @@ extern "C" bsgemm_status bsgemm_release_workspaces(void) {
     if (it->second.ws && cudaFree(it->second.ws) != cudaSuccess) st = BSGEMM_ERR_CUDA;
     if (it->second.counters && cudaFree(it->second.counters) != cudaSuccess) st = BSGEMM_ERR_CUDA;
     it = bsg_host::g_ws.erase(it);
+  }
+  for (auto it = bsg_host::g_outgrown.begin(); it != bsg_host::g_outgrown.end();) {
+    if (it->dev != cur) {
+      ++it;
+      continue;
+    }
+    if (cudaFree(it->p) != cudaSuccess) st = BSGEMM_ERR_CUDA;
+    it = bsg_host::g_outgrown.erase(it);
   }
   for (auto it = bsg_host::g_ids.begin(); it != bsg_host::g_ids.end();)
     it = it->first.first == cur ? bsg_host::g_ids.erase(it) : std::next(it);

@@ -50,7 +50,12 @@
  * exit.  A call captured into a CUDA graph can only use the workspace that
  * earlier uncaptured calls on the same stream made big enough; otherwise it
  * fails with BSGEMM_ERR_CUDA before anything is captured, and the capture
- * stays valid: run the same call once on that stream before capturing it.
+ * stays valid: run the same call once on that stream before capturing it.  A graph
+ * keeps using the workspace it was captured with: one that a graph uses and a
+ * later call outgrows stays allocated until bsgemm_release_workspaces(), after
+ * which no such graph may be replayed.  Graphs captured on one stream share its
+ * workspace with each other and with that stream's calls, so replay them in
+ * stream order with these, not at the same time on other streams.
  *
  * Alignment (TMA rules), checked on the host before any launch:
  *   a, b, out 16-byte aligned; scale_a, scale_b 4-byte aligned;

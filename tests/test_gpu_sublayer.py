@@ -495,6 +495,32 @@ def test_both_marshallings_agree(monkeypatch):
     assert fast.gemm(0, 128, x, x, w, w, None, 0, False, None) is None
 
 
+def test_a_captured_residual_gemm_outlives_the_growth_of_its_workspace():
+    """A stream-K call's graph, replayed after a larger call on its stream has taken a larger workspace."""
+    gen = gen_of(18)
+    bsg.release_workspaces()
+    a, b, sa, sb, _, _ = gemm_inputs(gen, 1, 2048, 4096, "nt", 128)
+    res = randn(gen, 1, 2048, dtype=torch.bfloat16)
+    assert bsg.make_plan(1, 2048, 4096, 128)["sk_ctas"] > 0
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        want = bsg.gemm(a, b, sa, sb, residual=res)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = bsg.gemm(a, b, sa, sb, residual=res)
+        big = gemm_inputs(gen, 128, 7168, 7168, "nt", 128)[:4]
+        first = bsg.gemm(*big)
+        for _ in range(20):
+            g.replay()
+            again = bsg.gemm(*big)
+        s.synchronize()
+    assert torch.equal(out, want) and torch.equal(first, again)
+    bsg.release_workspaces()
+    assert bsg.get_last_device_status() == 0
+
+
 FRESH_CAPTURE = """
 import torch
 import fp8_block_scaled_bsgemm_b200 as bsg
