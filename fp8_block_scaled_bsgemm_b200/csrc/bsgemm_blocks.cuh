@@ -49,11 +49,16 @@ struct BlockParams {
   int64_t rows, cols;
   int row_blocks, col_blocks;
   int step_rb, step_cb;   // from a CTA's block to its next: rows and columns of blocks
+  int backwards;          // rows of blocks are taken from the last to the first
 };
 
-// A walk over the matrix's blocks in row-major order, without divisions.
+// A walk over the matrix's blocks in row-major order, without divisions. rb
+// counts rows of blocks from the first taken; row() is the one meant.
 struct Walk {
   int rb, cb;
+  __device__ __forceinline__ int row(const BlockParams& p) const {
+    return p.backwards ? p.row_blocks - 1 - rb : rb;
+  }
   __device__ __forceinline__ void next(const BlockParams& p) {
     rb += p.step_rb;
     cb += p.step_cb;
@@ -119,11 +124,11 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
   uint32_t off[NP];
 #pragma unroll
   for (int j = 0; j < NP; ++j) off[j] = static_cast<uint32_t>(row0 + j * RP) * cols + col8;
-  auto first_of = [&](const Walk& w) { return static_cast<int64_t>(w.rb) * G * p.cols + w.cb * G; };
+  auto first_of = [&](const Walk& w) { return static_cast<int64_t>(w.row(p)) * G * p.cols + w.cb * G; };
   // row j * RP of the thread exists in block w if below this
-  auto left_of = [&](const Walk& w) { return w.cb * G + col8 < cols ? rows - w.rb * G - row0 : 0; };
+  auto left_of = [&](const Walk& w) { return w.cb * G + col8 < cols ? rows - w.row(p) * G - row0 : 0; };
   // the whole block lies inside the matrix
-  auto whole_of = [&](const Walk& w) { return (w.cb + 1) * G <= cols && rows - w.rb * G >= G; };
+  auto whole_of = [&](const Walk& w) { return (w.cb + 1) * G <= cols && rows - w.row(p) * G >= G; };
 
   bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
 
   Walk w{static_cast<int>(blockIdx.x / P) / p.col_blocks, static_cast<int>(blockIdx.x / P) % p.col_blocks};
   auto rows_of = [&](const Walk& at) {
-    return op.template rows<NP>(static_cast<int64_t>(at.rb) * G + row0, rows - at.rb * G - row0, RP);
+    return op.template rows<NP>(static_cast<int64_t>(at.row(p)) * G + row0, rows - at.row(p) * G - row0, RP);
   };
   if constexpr (kBuf > 0) fetch(w, 0);
   int par = 0;   // parity of the block: which copy of the exchanged values it uses
@@ -176,9 +181,9 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
     const int64_t first = first_of(w);
     const int left = left_of(w);
     const bool whole = whole_of(w);
-    const int64_t blk = static_cast<int64_t>(w.rb) * p.col_blocks + w.cb;
+    const int64_t blk = static_cast<int64_t>(w.row(p)) * p.col_blocks + w.cb;
     const int c0 = w.cb * G;
-    const int64_t part_row = static_cast<int64_t>(w.rb) * P + part;
+    const int64_t part_row = static_cast<int64_t>(w.row(p)) * P + part;
     const typename Op::template Rows<NP> of_rows = rows_of(w);
     const typename Op::Cols of_cols = op.cols(c0 + col8, left > 0);
     w.next(p);

@@ -401,6 +401,7 @@ bsgemm_status norm_of(int fmt, int gran, NormParams& p, cudaStream_t st, const b
   b.scales = p.scales;
   b.rows = p.rows;
   b.cols = p.cols;
+  b.backwards = 1;   // the rows written last are the likeliest still in L2
   return launch_blocks<BF16>(gran, fmt, b, Scaled{p.rstd, p.weight, p.weight_bf16}, st, dev);
 }
 
