@@ -30,19 +30,22 @@ using namespace bsgr;
 // cuts cross, so the work is done in two steps.
 //
 // Many rows: two kernels. The first streams the rows (h = x + residual, its
-// squares summed, rstd written) at the memory's rate: 30 us of the 53 us that
-// 8192 x 4096 BF16 with residual takes. The second reads h again, partly from
-// L2 (x and residual are read as first to leave it), and is the block kernel of
+// squares summed, rstd written) at the memory's rate: 30 us of the 50 us that
+// 8192 x 4096 BF16 with residual takes (0.71 of the copy rate over the bytes
+// that have to move). The second reads h again, partly from L2 (x and residual
+// are read as first to leave it, and its rows go from the last written to the
+// first: 70.2 -> 61.2 us at g = 256), and is the block kernel of
 // bsgemm_blocks.cuh with y = h * rstd * weight for a value. Slabs of rows whose
 // h stays in L2 whole cost more in extra launches than they save (32 MB slabs:
 // 58 us). One kernel that holds a row of blocks across a cluster of up to 16
 // CTAs, exchanging row sums through distributed shared memory between two
-// passes, took 57 us there and 14.7 against 5.6 us on 128 x 7168: its passes
+// passes, took 57 us there and 14.7 against 5.4 us on 128 x 7168: its passes
 // leave the memory idle at each barrier.
 //
 // Few rows (a decode step), where launches count: that one kernel, cut down to
 // rows that a CTA's threads take at once, with the values held in registers
-// between the passes.
+// between the passes. A row of 7168 BF16 takes 3.7 us: the launch, two trips to
+// memory and the cluster's two barriers.
 
 struct NormParams {
   const void* x;
@@ -414,7 +417,10 @@ bsgemm_status norm_of(int fmt, int gran, NormParams& p, cudaStream_t st, const b
 // keeps the sums of dy * n of its 16 columns over all its rows; at the end they
 // are added over the CTA's row groups and written as one row of partial sums,
 // and a second kernel adds those rows in order (no atomics: the order never
-// changes).
+// changes). B200, BF16 with the skip path's gradient: 8192 x 4096 50.1 us (0.81
+// of the copy rate over the bytes that have to move), where a barrier a row and
+// the sums at the end show, 32768 x 4096 167 us (0.98). Without the next row's
+// runs under way during a row's sum the first took 58.1 us.
 
 constexpr int kBwdMaxThreads = 512;
 constexpr int kBwdRuns = 2;          // runs to a thread, TC * 8 columns apart
