@@ -11,6 +11,7 @@
 #include <iterator>
 #include <map>
 #include <mutex>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -130,7 +131,7 @@ bsgemm_status device_info(DeviceInfo& out) {
 // only use the workspace an uncaptured call on the same stream already made
 // big enough (the graph would otherwise own the new memory); otherwise it
 // fails with BSGEMM_ERR_CUDA before anything is captured.
-bsgemm_status get_workspace(cudaStream_t stream, size_t ws_bytes, size_t n_counters, Workspace& out) {
+bsgemm_status get_workspace(cudaStream_t stream, size_t ws_bytes, size_t n_counters, Workspace& out) try {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return BSGEMM_ERR_CUDA;
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
@@ -177,6 +178,8 @@ bsgemm_status get_workspace(cudaStream_t stream, size_t ws_bytes, size_t n_count
   if (capturing) w.in_graph = true;
   out = w;
   return BSGEMM_OK;
+} catch (const std::bad_alloc&) {   // of the host's maps
+  return BSGEMM_ERR_CUDA;
 }
 
 unsigned long long wait_timeout_ns() {

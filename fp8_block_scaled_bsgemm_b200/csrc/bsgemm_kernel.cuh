@@ -498,7 +498,7 @@ __device__ __forceinline__ void apply_epi_staged(const Params& p, uint32_t buf, 
 #pragma unroll
     for (int i = 0; i < 2 * NP / 32; ++i) {
       const int n = n0 + 32 * i + static_cast<int>(lane);
-      b[i] = __ldg(p.bias + (n < p.N ? n : 0));
+      b[i] = __ldca(p.bias + (n < p.N ? n : 0));
     }
     if (lane == 0) bulk_wait_group_read0();
     __syncwarp();
@@ -566,6 +566,7 @@ template <int NP, bool F32>
 struct ResidualChunks {
   static constexpr int kCols = F32 ? 32 : 64;   // columns per chunk
   static constexpr int kChunks = 2 * NP / kCols;
+  static_assert(kChunks >= 1 && 2 * NP % kCols == 0, "a warp's columns are whole chunks");
 
   // The previous store must have finished reading the buffer, and every lane
   // the chunk before this one: each lane's fence holds its reads (and stores)
@@ -1402,7 +1403,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
           named_barrier_sync(2, kNumEpiThreads);
           const uint32_t col0 = stage + (half * kHalf * BM + row_in_tile) * 2;  // m = half * kHalf
           if constexpr (EPI) {
-            const float bn = (p.bias != nullptr && n < p.N) ? __ldg(p.bias + n) : 0.f;
+            const float bn = (p.bias != nullptr && n < p.N) ? __ldca(p.bias + n) : 0.f;
             with_act(p.epi & 3, [&](auto tag) {
               constexpr int ACT = decltype(tag)::value;
 #pragma unroll
@@ -1431,7 +1432,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
             if (m < p.M) reinterpret_cast<float*>(p.out)[static_cast<size_t>(m) * p.N + n] = v;
           };
           if constexpr (EPI) {
-            const float bn = p.bias != nullptr ? __ldg(p.bias + n) : 0.f;
+            const float bn = p.bias != nullptr ? __ldca(p.bias + n) : 0.f;
             with_act(p.epi & 3, [&](auto tag) {
               constexpr int ACT = decltype(tag)::value;
 #pragma unroll

@@ -67,15 +67,16 @@ struct NormParams {
 };
 
 __device__ __forceinline__ void load_weight(const void* weight, int is_bf16, int64_t c, float2 (&w)[4]) {
-  // (an input only, read for every row: kept in L1)
+  // (read for every row: kept in L1; not by a read-only load, since the kernel
+  // may begin while the one that writes the weight still runs)
   if (is_bf16) {
     Run<true> r;
-    r.w[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(weight) + c));
+    r.w[0] = __ldca(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(weight) + c));
     widen<true>(r, w);
   } else {
     Run<false> r;
-    r.w[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(weight) + c));
-    r.w[1] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(weight) + c) + 1);
+    r.w[0] = __ldca(reinterpret_cast<const uint4*>(static_cast<const float*>(weight) + c));
+    r.w[1] = __ldca(reinterpret_cast<const uint4*>(static_cast<const float*>(weight) + c) + 1);
     widen<false>(r, w);
   }
 }

@@ -265,8 +265,10 @@ bsgemm_status bsgemm_fp8_gemm_fused(int layout, int a_format, int b_format, cons
 /* bsgemm_fp8_gemm_fused that also adds a residual, after the activation:
  *   out[m,n] = act(acc[m,n] + bias[n]) + residual[m,n]
  * residual is [M,N] row-major in out's type (epi's out_dtype, BF16 without
- * epi), 16-byte aligned. The sum is taken in FP32 and rounded once. residual
- * may be out itself (the residual stream updated in place); any other overlap
+ * epi), 16-byte aligned. The sum is taken in FP32 and rounded once to out's
+ * type (without an activation the residual may join the sum over K before its
+ * last blocks do, so an FP32 out can differ in its last places from a residual
+ * added last). residual may be out itself (the residual stream updated in place); any other overlap
  * of the two is BSGEMM_ERR_INVALID_ARG, and so is a NULL residual. With split-K
  * or stream-K the residual is added once, after the pieces are summed.
  * Everything else as bsgemm_fp8_gemm_fused. Gradients: the residual's is that
@@ -282,8 +284,9 @@ bsgemm_status bsgemm_fp8_gemm_residual(int layout, int a_format, int b_format, c
  * The steps between two GEMMs of a transformer sublayer, each fused with the
  * quantisation of its result into the next GEMM's operand. Shared rules:
  *   - matrices are dense row-major [rows, cols], rows in 1 .. 2^30, cols in
- *     1 .. 2^24 (else BSGEMM_ERR_INVALID_ARG), cols % 16 == 0 (else BSGEMM_ERR_MISALIGNED), of src_dtype (FP32 or BF16;
- *     one type for all of a call's matrices), device pointers 16-byte aligned;
+ *     1 .. 2^24 (else BSGEMM_ERR_INVALID_ARG), cols % 16 == 0 (else
+ *     BSGEMM_ERR_MISALIGNED), of src_dtype (FP32 or BF16; one type for all of a
+ *     call's matrices), device pointers 16-byte aligned;
  *   - q, scales, gran and fp8_format are the quantiser's (above), except that
  *     a block whose amax / FMAX rounds to 0 also gets scale 1. Values are
  *     quantised as computed in FP32, without a rounding to src_dtype between;
