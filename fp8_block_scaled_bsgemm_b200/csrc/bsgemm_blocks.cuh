@@ -30,9 +30,9 @@ template <int G>
 constexpr int kCtasPerSm = G == 64 ? 4 : 2;
 
 // A thread's runs of a block pass through shared memory (cp.async into places
-// that this thread alone reads, so no barrier is needed), which keeps the next
-// block's loads in flight while this one is computed without holding them in
-// registers. Two buffers where they fit beside a second CTA, else one, refilled
+// that its warp alone reads, so no barrier of the CTA is needed), which keeps
+// the next block's loads in flight while this one is computed without holding
+// them in registers. Two buffers where they fit beside a second CTA, else one, refilled
 // once the block's values are in registers; none for the widest case.
 template <int G, bool BF16, bool IN2>
 constexpr int kBufBytes = kThreads<G> * (G / kParts<G> / (kThreads<G> / (G / kVec))) * (BF16 ? 16 : 32) * (IN2 ? 2 : 1);
@@ -69,19 +69,47 @@ struct Walk {
   }
 };
 
-// Copies a run into shared memory, zeros (and no access) where it lies outside
-// the matrix (WHOLE: it does not).
-template <bool BF16, bool WHOLE>
-__device__ __forceinline__ void fetch_run(uint32_t dst, const char* src, bool in) {
-#pragma unroll
-  for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
-    if constexpr (WHOLE)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * h), "l"(src + 16 * h) : "memory");
-    else
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * h), "l"(src + (in ? 16 * h : 0)),
-                   "r"(in ? 16 : 0)
-                   : "memory");
+// Copies 16 bytes into shared memory, zeros (and no access) where they lie
+// outside the matrix (WHOLE: they do not).
+template <bool WHOLE>
+__device__ __forceinline__ void fetch16(uint32_t dst, const char* src, bool in) {
+  if constexpr (WHOLE)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+// One run for each of L neighbouring threads, at `dst` + 16 bytes a thread. A
+// BF16 run is 16 bytes and its thread copies it. An FP32 run is two halves; if
+// its thread copied both, each copy of a warp would touch half of every 32-byte
+// sector and fetch it twice. So the group's 2 L halves are copied in order,
+// thread i taking halves i and i + L (L * 16 bytes on), and lie apart by parity:
+// first halves in T * 16 bytes, then second halves, in places flipped by 4 so
+// that neither the copies nor the reads meet in a bank. `src` is the thread's
+// first 16 bytes, `in` and `in2` whether its pieces exist.
+template <bool BF16, bool WHOLE, int T, int L>
+__device__ __forceinline__ void fetch_run(uint32_t dst, int tid, const char* src, bool in, bool in2) {
+  if constexpr (BF16) {
+    fetch16<WHOLE>(dst + tid * 16, src, in);
+  } else {
+    static_assert(L >= 8 && L <= 32, "a group lies within a warp");
+    dst += (tid - tid % L) * 32 + tid % L * 16;
+    fetch16<WHOLE>(dst, src, in);
+    fetch16<WHOLE>(dst + L * 16, src + (in2 || WHOLE ? L * 16 : 0), in2);
   }
+}
+// The thread's run, past fetch_wait (and a __syncwarp for FP32).
+template <bool BF16, int T>
+__device__ __forceinline__ Run<BF16> fetched_run(const uint4* at, int tid) {
+  Run<BF16> r;
+  if constexpr (BF16) {
+    r.w[0] = at[tid];
+  } else {
+    const int flip = (tid >> 2) & 1;
+    const uint4 x = at[2 * tid + flip], y = at[2 * tid + (flip ^ 1)];
+    r.w[0] = flip ? y : x;
+    r.w[1] = flip ? x : y;
+  }
+  return r;
 }
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -124,6 +152,8 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
   uint32_t off[NP];
 #pragma unroll
   for (int j = 0; j < NP; ++j) off[j] = static_cast<uint32_t>(row0 + j * RP) * cols + col8;
+  // the first column that the thread copies: its own run's for BF16, see fetch_run
+  const int copy_col = BF16 ? col8 : col8 / 2;
   auto first_of = [&](const Walk& w) { return static_cast<int64_t>(w.row(p)) * G * p.cols + w.cb * G; };
   // row j * RP of the thread exists in block w if below this
   auto left_of = [&](const Walk& w) { return w.cb * G + col8 < cols ? rows - w.row(p) * G - row0 : 0; };
@@ -133,42 +163,39 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
   bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
 
-  const uint32_t own = kBuf > 0 ? bsg::smem_addr(fetched) + tid * kRun : 0;
+  const uint32_t runs = kBuf > 0 ? bsg::smem_addr(fetched) : 0;
   auto slot = [&](int buf, int input, int j) -> uint32_t {
-    return own + ((buf * (IN2 ? 2 : 1) + input) * NP + j) * (T * kRun);
+    return runs + ((buf * (IN2 ? 2 : 1) + input) * NP + j) * (T * kRun);
   };
   const char* in0 = static_cast<const char*>(p.in0);
   const char* in1 = static_cast<const char*>(p.in1);
   auto fetch = [&](const Walk& w, int buf) {
     if (w.rb < p.row_blocks) {
-      const int64_t first = first_of(w);
+      const int64_t first = first_of(w) - (col8 - copy_col);
       const char* src0 = in0 + first * kElem;
       const char* src1 = in1 + (IN2 ? first * kElem : 0);
       if (whole_of(w)) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          fetch_run<BF16, true>(slot(buf, 0, j), src0 + static_cast<uint64_t>(off[j]) * kElem, true);
-          if constexpr (IN2) fetch_run<BF16, true>(slot(buf, 1, j), src1 + static_cast<uint64_t>(off[j]) * kElem, true);
+          const uint64_t e = static_cast<uint64_t>(off[j]) * kElem;
+          fetch_run<BF16, true, T, L>(slot(buf, 0, j), tid, src0 + e, true, true);
+          if constexpr (IN2) fetch_run<BF16, true, T, L>(slot(buf, 1, j), tid, src1 + e, true, true);
         }
       } else {
-        const int left = left_of(w);
+        const int c = w.cb * G + copy_col, left = rows - w.row(p) * G - row0;
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          const bool in = j * RP < left;
-          const uint64_t e = in ? static_cast<uint64_t>(off[j]) * kElem : 0;
-          fetch_run<BF16, false>(slot(buf, 0, j), src0 + e, in);
-          if constexpr (IN2) fetch_run<BF16, false>(slot(buf, 1, j), src1 + e, in);
+          const bool in = j * RP < left && c < cols, in2 = j * RP < left && c + L * 4 < cols;
+          const uint64_t e = static_cast<uint64_t>(off[j]) * kElem;
+          fetch_run<BF16, false, T, L>(slot(buf, 0, j), tid, in ? src0 + e : in0, in, in2);
+          if constexpr (IN2) fetch_run<BF16, false, T, L>(slot(buf, 1, j), tid, in ? src1 + e : in1, in, in2);
         }
       }
     }
     fetch_commit();
   };
-  auto fetched_run = [&](int buf, int input, int j) {
-    Run<BF16> r;
-    const uint4* at = fetched + (((buf * (IN2 ? 2 : 1) + input) * NP + j) * T + tid) * (kRun / 16);
-#pragma unroll
-    for (int h = 0; h < (BF16 ? 1 : 2); ++h) r.w[h] = at[h];
-    return r;
+  auto fetched_of = [&](int buf, int input, int j) {
+    return fetched_run<BF16, T>(fetched + ((buf * (IN2 ? 2 : 1) + input) * NP + j) * (T * kRun / 16), tid);
   };
 
   Walk w{static_cast<int>(blockIdx.x / P) / p.col_blocks, static_cast<int>(blockIdx.x / P) % p.col_blocks};
@@ -194,14 +221,15 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
     } else if constexpr (kBuf == 1) {
       fetch_wait<0>();
     }
+    if constexpr (!BF16 && kBuf > 0) __syncwarp();   // the warp's other threads' copies
     float2 v[NP][4];
     float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       Run<BF16> a, b;
       if constexpr (kBuf > 0) {
-        a = fetched_run(buf, 0, j);
-        if constexpr (IN2) b = fetched_run(buf, 1, j);
+        a = fetched_of(buf, 0, j);
+        if constexpr (IN2) b = fetched_of(buf, 1, j);
       } else {
         a = b = zero_run<BF16>();
         if (j * RP < left) {

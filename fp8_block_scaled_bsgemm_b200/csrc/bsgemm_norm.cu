@@ -486,48 +486,57 @@ __global__ void __launch_bounds__(T, kBwdCtasPerSm<T, BF16>)
   int64_t e = r * p.cols + c0;
   const int64_t e_step = stride * p.cols;
   // A thread's runs of the next row pass through places in shared memory that
-  // it alone reads (cp.async, two rows' worth), so that loads are in flight
-  // through this row's barrier and arithmetic.
+  // its warp alone reads (cp.async, two rows' worth), so that loads are in
+  // flight through this row's barrier and arithmetic.
   constexpr int kRun = BF16 ? 16 : 32, kElem = BF16 ? 2 : 4, kInputs = SKIP ? 3 : 2;
-  const uint32_t own = bsg::smem_addr(fetched) + tid * kRun;
+  // the first column that the thread copies, from its own run's (see fetch_run)
+  const int copy = BF16 ? 0 : -(lane * 4);
+  bool copied[V], copied2[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = run0 + copy + v * tc * kVec, c2 = c + 32 * 4;
+    const int64_t slice0 = c0 - run0;
+    copied[v] = c < p.slice && slice0 + c < p.cols;
+    copied2[v] = c2 < p.slice && slice0 + c2 < p.cols;
+  }
+  const uint32_t runs = bsg::smem_addr(fetched);
   auto fetch = [&](int64_t row, int64_t at, int to) {
     if (row < p.rows) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (!in[v]) continue;
-        const int64_t o = (at + v * tc * kVec) * kElem;
+        if (BF16 ? !in[v] : !copied[v]) continue;   // (a second piece lies behind the first)
+        const int64_t o = (at + copy + v * tc * kVec) * kElem;
         const char* src[3] = {static_cast<const char*>(p.dy), static_cast<const char*>(p.h),
                               static_cast<const char*>(p.skip)};
 #pragma unroll
         for (int k = 0; k < kInputs; ++k)
-          fetch_run<BF16, true>(own + ((to * kInputs + k) * V + v) * (T * kRun), src[k] + o, true);
+          fetch_run<BF16, BF16, T, 32>(runs + ((to * kInputs + k) * V + v) * (T * kRun), tid, src[k] + o, true,
+                                       copied2[v]);
       }
     }
     fetch_commit();
   };
-  auto fetched_run = [&](int from, int input, int v) {
-    Run<BF16> x;
-    const uint4* at = fetched + (((from * kInputs + input) * V + v) * T + tid) * (kRun / 16);
-#pragma unroll
-    for (int k = 0; k < (BF16 ? 1 : 2); ++k) x.w[k] = at[k];
-    return x;
+  auto fetched_of = [&](int from, int input, int v) {
+    return fetched_run<BF16, T>(fetched + ((from * kInputs + input) * V + v) * (T * kRun / 16), tid);
   };
   int buf = 0;
   fetch(r, e, 0);
   float rs_next = r < p.rows ? __ldcg(p.rstd + r) : 0.f;
   for (int64_t base = static_cast<int64_t>(part) * groups; base < p.rows; base += stride) {
     const bool exists = r < p.rows;
+    if constexpr (!BF16) __syncwarp();   // the warp has read the buffer's last row
     fetch(r + stride, e + e_step, buf ^ 1);
     const float rs = rs_next;
     rs_next = r + stride < p.rows ? __ldcg(p.rstd + r + stride) : 0.f;
     fetch_wait<1>();
+    if constexpr (!BF16) __syncwarp();   // the warp's other threads' copies
     float2 s2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (!in[v] || !exists) continue;
       float2 a[4], b[4];
-      widen<BF16>(fetched_run(buf, 0, v), a);
-      widen<BF16>(fetched_run(buf, 1, v), b);
+      widen<BF16>(fetched_of(buf, 0, v), a);
+      widen<BF16>(fetched_of(buf, 1, v), b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 n = mul2(b[i], both(rs));
@@ -559,15 +568,15 @@ __global__ void __launch_bounds__(T, kBwdCtasPerSm<T, BF16>)
     for (int v = 0; v < V; ++v) {
       if (!in[v] || !exists) continue;
       float2 a[4], b[4];
-      widen<BF16>(fetched_run(buf, 0, v), a);
-      widen<BF16>(fetched_run(buf, 1, v), b);
+      widen<BF16>(fetched_of(buf, 0, v), a);
+      widen<BF16>(fetched_of(buf, 1, v), b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 n = mul2(b[i], both(rs));
         a[i] = mul2(bsg::ffma2(n, both(-m), mul2(a[i], w[v][i])), both(rs));
       }
       if constexpr (SKIP) {
-        widen<BF16>(fetched_run(buf, 2, v), b);
+        widen<BF16>(fetched_of(buf, 2, v), b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = add2(a[i], b[i]);
       }

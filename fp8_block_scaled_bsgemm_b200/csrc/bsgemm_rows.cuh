@@ -35,15 +35,15 @@ __device__ __forceinline__ Run<BF16> zero_run() {
   return r;
 }
 
-// Loads go through L2 only (ld.global.cg): each run is read once per pass, and
-// where an output may be the same buffer as an input no stale line can stay
-// in L1.
+// BF16 runs are loaded through L2 only: each is read once per pass. An FP32 run
+// takes two loads, each of which touches half of every 32-byte sector, so the
+// second finds its half in L1.
 template <bool BF16>
 __device__ __forceinline__ Run<BF16> load_run(const void* base, int64_t elem) {
   Run<BF16> r;
   const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + elem * (BF16 ? 2 : 4));
 #pragma unroll
-  for (int h = 0; h < (BF16 ? 1 : 2); ++h) r.w[h] = __ldcg(p + h);
+  for (int h = 0; h < (BF16 ? 1 : 2); ++h) r.w[h] = BF16 ? __ldcg(p + h) : __ldca(p + h);
   return r;
 }
 
