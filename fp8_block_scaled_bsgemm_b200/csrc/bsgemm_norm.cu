@@ -430,7 +430,7 @@ bsgemm_status norm_of(int fmt, int gran, NormParams& p, cudaStream_t st, const b
 // keeps the sums of dy * n of its 16 columns over all its rows; at the end they
 // are added over the CTA's row groups and written as one row of partial sums,
 // and a second kernel adds those rows in order (no atomics: the order never
-// changes). B200, BF16 with the skip path's gradient: 8192 x 4096 50.1 us (0.81
+// changes). B200, BF16 with the skip path's gradient: 8192 x 4096 49.0 us (0.83
 // of the copy rate over the bytes that have to move), where a barrier a row and
 // the sums at the end show, 32768 x 4096 167 us (0.98). Without the next row's
 // runs under way during a row's sum the first took 58.1 us.
@@ -626,16 +626,25 @@ __global__ void __launch_bounds__(T, kBwdCtasPerSm<T, BF16>)
 }
 
 // One CTA adds 32 columns: 32 warps take every 32nd row, then one warp adds
-// the 32 sums in order.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int parts, int64_t cols, float* out) {
+// the 32 sums in order. The loads of kSumRows rows are in flight at once (20 of
+// them took 52 registers, which kept the CTAs out until the last kernel's had
+// left: 333 x 1552 7.1 against 5.2 us).
+constexpr int kSumRows = 5;
+__global__ void __launch_bounds__(1024, 2) column_sum_kernel(const float* part, int parts, int64_t cols, float* out) {
   __shared__ float sums[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   bsg::grid_dependency_wait();
   float s = 0.f;
   if (c < cols) {
-#pragma unroll 4
-    for (int i = warp; i < parts; i += 32) s += __ldcg(part + static_cast<int64_t>(i) * cols + c);
+    for (int i = warp; i < parts; i += 32 * kSumRows) {
+      float v[kSumRows];
+#pragma unroll
+      for (int k = 0; k < kSumRows; ++k)
+        v[k] = i + 32 * k < parts ? __ldcg(part + static_cast<int64_t>(i + 32 * k) * cols + c) : 0.f;
+#pragma unroll
+      for (int k = 0; k < kSumRows; ++k) s += v[k];
+    }
   }
   sums[warp][lane] = s;
   __syncthreads();
