@@ -9,7 +9,7 @@
 //            the two gradient products), dbias[n] = sum over rows of dz.
 //            The residual's gradient is dout itself.
 // Both run in the block kernel of bsgemm_blocks.cuh. B200, 8192 x 14336 BF16,
-// g = 128: GELU 67.6 us (0.79 of the copy rate), its gradient with dbias 109 us
+// g = 128: GELU 66.7 us (0.80 of the copy rate), its gradient with dbias 109 us
 // (0.82), both held by instruction issue (two thirds of the slots taken); ReLU
 // is at the memory's rate (8192 x 8192: 30.6 us).
 #include "bsgemm_blocks.cuh"
