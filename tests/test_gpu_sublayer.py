@@ -38,7 +38,7 @@ def check_norm(x, w, residual, gran, fmt, result):
 
 
 @pytest.mark.parametrize("gran", [64, 128, 256])
-@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 7168), (2, 1040), (9, 208), (33, 4112), (64, 64), (130, 1296), (300, 528),
+@pytest.mark.parametrize("rows,cols", [(1, 16), (70, 1072), (70, 1264), (1, 7168), (2, 1040), (9, 208), (33, 4112), (64, 64), (130, 1296), (300, 528),
                                        (257, 2064), (5, 40016)])
 @pytest.mark.parametrize("dtype,with_residual,fmt", [(torch.bfloat16, True, "e4m3"), (torch.bfloat16, False, "e5m2"),
                                                      (torch.float32, True, "e5m2"), (torch.float32, False, "e4m3")])
@@ -137,7 +137,7 @@ def check_norm_backward(dy, h, w, rstd, skip, dx, dw):
     assert ((dw.double() - want_dw).abs() <= tol).all(), float(((dw.double() - want_dw).abs() / tol).max())
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 7168), (2, 208), (7, 272), (333, 1552), (1200, 4096), (600, 4112), (40, 16400),
+@pytest.mark.parametrize("rows,cols", [(1, 16), (70, 1072), (21, 1264), (1, 7168), (2, 208), (7, 272), (333, 1552), (1200, 4096), (600, 4112), (40, 16400),
                                        (9, 65536), (5000, 64)])
 @pytest.mark.parametrize("dtype,with_skip", [(torch.bfloat16, True), (torch.bfloat16, False), (torch.float32, True),
                                              (torch.float32, False)])
@@ -190,7 +190,7 @@ def test_norm_backward_against_differences():
 
 
 @pytest.mark.parametrize("gran", [64, 128, 256])
-@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 14336), (8, 272), (130, 1040), (300, 528), (257, 64)])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (70, 1072), (70, 1264), (1, 14336), (8, 272), (130, 1040), (300, 528), (257, 64)])
 @pytest.mark.parametrize("dtype,act,fmt", [(torch.bfloat16, "gelu", "e4m3"), (torch.bfloat16, "relu", "e5m2"),
                                            (torch.float32, "gelu", "e5m2"), (torch.float32, "relu", "e4m3")])
 def test_activation_quantize(gran, rows, cols, dtype, act, fmt):
@@ -219,7 +219,7 @@ def test_gelu_over_every_bf16_value():
 
 
 @pytest.mark.parametrize("gran", [64, 128, 256])
-@pytest.mark.parametrize("rows,cols", [(1, 16), (3, 14336), (130, 1040), (300, 528), (777, 64)])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (70, 1072), (70, 1264), (3, 14336), (130, 1040), (300, 528), (777, 64)])
 @pytest.mark.parametrize("dtype,act,fmt", [(torch.bfloat16, "gelu", "e5m2"), (torch.bfloat16, "relu", "e4m3"),
                                            (torch.float32, "gelu", "e4m3"), (torch.float32, None, "e5m2"),
                                            (torch.bfloat16, "none", "e4m3")])
