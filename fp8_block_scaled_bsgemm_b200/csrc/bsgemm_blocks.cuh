@@ -279,11 +279,7 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
     uint8_t* q = p.q + first;
     if (whole && s.rcp > 0.f) {
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], both(s.rcp));
-        store_codes<FMT>(q + off[j], v[j]);
-      }
+      for (int j = 0; j < NP; ++j) store_codes<FMT, true>(q + off[j], v[j], s);
     } else {
 #pragma unroll
       for (int j = 0; j < NP; ++j)

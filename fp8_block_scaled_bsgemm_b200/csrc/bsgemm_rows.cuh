@@ -137,13 +137,16 @@ constexpr float kFmax = FMT == BSGEMM_FP8_E5M2 ? 57344.0f : 448.0f;
 // A block's scale and its reciprocal, each thread for itself.
 //   s = RN(amax / FMAX), or 1 where that is 0 (an empty block, or one whose
 //       amax / FMAX is below the smallest FP32 value);
-//   rcp = 1 / s to within FP32's last place, or 0 where amax lies outside the
-//       range that makes both quotients safe (the codes then take divisions).
+//   rcp = RN(1 / s), or 0 where amax lies outside the range that makes both
+//       quotients safe (the codes then take divisions).
 // The quotient by the constant is the product with its rounded reciprocal and
 // one correction by the exact remainder (Markstein): correctly rounded where
 // neither the quotient nor the remainder is near FP32's smallest values, which
-// the threshold keeps away; below it the division itself.
-constexpr float kSmallAmax = 0x1p-80f;
+// the threshold keeps away; below it the division itself. The threshold keeps
+// quotients()'s remainders exact too: a quotient that is not below every border
+// between codes is at least 2^-17 (E5M2; E4M3 2^-10), so its value is at least
+// 2^-17 * 2^-64 / 57344 > 2^-97, whose remainder is a multiple of 2^-145.
+constexpr float kSmallAmax = 0x1p-64f;
 
 struct Scale {
   float s, rcp;
@@ -156,13 +159,28 @@ __device__ __forceinline__ Scale block_scale(float amax) {
   if (amax >= kSmallAmax && amax < 0x1p127f) {
     const float q = amax * inv;
     r.s = __fmaf_rn(__fmaf_rn(-q, kFmax<FMT>, amax), inv, q);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.rcp) : "f"(r.s));
+    r.rcp = __frcp_rn(r.s);
   } else {
     const float q = __fdiv_rn(amax, kFmax<FMT>);
     r.s = q > 0.f ? q : 1.f;
     r.rcp = q > 0.f ? 0.f : 1.f;
   }
   return r;
+}
+
+// v / s of a run, negated, where s.rcp > 0: the product with the reciprocal and
+// Markstein's correction by its remainder, whose FP8 codes are those of the
+// correctly rounded quotients (tests/block_quotient_model.c: every scale beside
+// every border between codes). With the product alone a value beside a border
+// could take the code on the border's other side. The signs are turned so that a
+// zero keeps its own without a negation per value; the code's bit is turned back.
+__device__ __forceinline__ void quotients(float2 (&v)[4], const Scale& s) {
+  const float2 nr = both(-s.rcp);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = mul2(v[i], nr);
+    v[i] = bsg::ffma2(bsg::ffma2(p, both(s.s), v[i]), nr, p);
+  }
 }
 
 // FP8 codes of four values, the first in the lowest byte: round to nearest even,
@@ -186,26 +204,19 @@ __device__ __forceinline__ uint32_t encode4(float2 a, float2 b) {
   return r;
 }
 
-// Stores the codes of a run of quotients.
-template <int FMT>
-__device__ __forceinline__ void store_codes(uint8_t* q, const float2 (&v)[4]) {
-  *reinterpret_cast<uint2*>(q) = make_uint2(encode4<FMT>(v[0], v[1]), encode4<FMT>(v[2], v[3]));
-}
-
-// Stores the codes of v / s. The quotient is v times the reciprocal of s:
-// within 2 units of FP32's last place of the divided value, which is itself
-// that far from the exact one, against a code's half step of 2^-4.
-template <int FMT>
-__device__ __forceinline__ void store_codes(uint8_t* q, const float2 (&v)[4], const Scale& s) {
-  float2 d[4];
-  if (s.rcp > 0.f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = mul2(v[i], both(s.rcp));
+// Stores the codes of v / s where s.rcp > 0 (WHOLE: the caller knows), else by
+// divisions.
+template <int FMT, bool WHOLE = false>
+__device__ __forceinline__ void store_codes(uint8_t* q, float2 (&v)[4], const Scale& s) {
+  uint32_t sign = 0;
+  if (WHOLE || s.rcp > 0.f) {
+    quotients(v, s);
+    sign = 0x80808080u;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = make_float2(__fdiv_rn(v[i].x, s.s), __fdiv_rn(v[i].y, s.s));
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__fdiv_rn(v[i].x, s.s), __fdiv_rn(v[i].y, s.s));
   }
-  store_codes<FMT>(q, d);
+  *reinterpret_cast<uint2*>(q) = make_uint2(encode4<FMT>(v[0], v[1]) ^ sign, encode4<FMT>(v[2], v[3]) ^ sign);
 }
 
 // Largest of a (not negative) and the run's magnitudes, two values to an
