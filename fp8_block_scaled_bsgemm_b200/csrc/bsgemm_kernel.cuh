@@ -287,7 +287,8 @@ struct WorkIter {
 
 // Grouped GEMM: advance the cursor to the group that holds tile it.wi (tiles
 // are numbered group by group; each group has ceil(rows / 128) x tiles_q).
-// Returns false once every group is used up.
+// Returns false once every group is used up. (The sizes are not read by
+// read-only loads: their writer may still run when this kernel begins.)
 template <int GRAN>
 __device__ __forceinline__ bool group_seek(const Params& p, WorkIter& it) {
   while (it.wi >= it.g_first + it.g_tiles) {
@@ -295,7 +296,7 @@ __device__ __forceinline__ bool group_seek(const Params& p, WorkIter& it) {
     it.g_row += it.g_m;
     it.g_srow += (it.g_m + GRAN - 1) / GRAN;
     if (++it.g >= p.num_groups) return false;
-    it.g_m = max(0, __ldg(p.group_m + it.g));
+    it.g_m = max(0, __ldca(p.group_m + it.g));
     it.g_tiles = (it.g_m + BM - 1) / BM * p.tiles_q;
   }
   return true;
@@ -311,7 +312,7 @@ __device__ __forceinline__ void work_begin(const Params& p, WorkIter& it) {
     it.g_first = 0;
     it.g_row = 0;
     it.g_srow = 0;
-    it.g_m = max(0, __ldg(p.group_m));
+    it.g_m = max(0, __ldca(p.group_m));
     it.g_tiles = (it.g_m + BM - 1) / BM * p.tiles_q;
   }
 }
@@ -1193,10 +1194,12 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       auto load_chunk = [&](int base, float (&dst)[kNumGroups]) {
         const int kb = base + static_cast<int>(lane);
         const bool in = kb < w.kb1;
-        const float a = in ? __ldg(sp_row + kb) : 0.f;
+        // (not by read-only loads: this kernel may begin while the one that
+        // writes the scales, the norm or the activation in front of it, still runs)
+        const float a = in ? __ldcg(sp_row + kb) : 0.f;
 #pragma unroll
         for (int j = 0; j < kNumGroups; ++j)
-          dst[j] = in ? a * __ldg(p.sQ + static_cast<size_t>(qb[j]) * p.Kb + kb) : 0.f;
+          dst[j] = in ? a * __ldcg(p.sQ + static_cast<size_t>(qb[j]) * p.Kb + kb) : 0.f;
       };
       load_chunk(w.kb0, sc_cur);
       load_chunk(w.kb0 + 32, sc_nxt);

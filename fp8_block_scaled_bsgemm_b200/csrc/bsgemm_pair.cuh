@@ -319,10 +319,11 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       auto load_chunk = [&](int base, float (&dst)[kNumGroups]) {
         const int kb = base + static_cast<int>(lane);
         const bool in = kb < p.Kb;
-        const float a = in ? __ldg(sp_row + kb) : 0.f;
+        // (not by read-only loads, as in bsgemm_kernel)
+        const float a = in ? __ldcg(sp_row + kb) : 0.f;
 #pragma unroll
         for (int j = 0; j < kNumGroups; ++j)
-          dst[j] = in ? a * __ldg(p.sQ + static_cast<size_t>(qb[j]) * p.Kb + kb) : 0.f;
+          dst[j] = in ? a * __ldcg(p.sQ + static_cast<size_t>(qb[j]) * p.Kb + kb) : 0.f;
       };
       load_chunk(0, sc_cur);
       load_chunk(32, sc_nxt);
