@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
   // the whole block lies inside the matrix
   auto whole_of = [&](const Walk& w) { return (w.cb + 1) * G <= cols && rows - w.row(p) * G >= G; };
 
+  if constexpr (P > 1) bsg::cluster_open_arrive();
   bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
 
@@ -203,6 +204,7 @@ __global__ void __launch_bounds__(kThreads<G>, kCtasPerSm<G>)
     return op.template rows<NP>(static_cast<int64_t>(at.row(p)) * G + row0, rows - at.row(p) * G - row0, RP);
   };
   if constexpr (kBuf > 0) fetch(w, 0);
+  if constexpr (P > 1) bsg::cluster_open_wait();
   int par = 0;   // parity of the block: which copy of the exchanged values it uses
   for (; w.rb < p.row_blocks; par ^= 1) {
     const int64_t first = first_of(w);

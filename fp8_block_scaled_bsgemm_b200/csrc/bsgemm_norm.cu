@@ -45,7 +45,8 @@ using namespace bsgr;
 // Few rows (a decode step), where launches count: that one kernel, cut down to
 // rows that a CTA's threads take at once, with the values held in registers
 // between the passes. A row of 7168 BF16 takes 3.7 us: the launch, two trips to
-// memory and the cluster's two barriers.
+// memory and the cluster's barrier (a second one, which opens the cluster, ends
+// under the first loads).
 
 struct NormParams {
   const void* x;
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(kFewThreads) norm_few_kernel(const __grid_cons
   const int step = p.cluster * slots;      // col_blocks + K * step stays far below 2^31
   const int64_t base = rr * p.cols + col8;
 
+  if (p.cluster > 1) bsg::cluster_open_arrive();
   for (int i = tid; i < 3 * K * RP; i += kFewThreads) (&block_max[0][0][0])[i] = 0;
   bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
@@ -289,6 +291,7 @@ __global__ void __launch_bounds__(kFewThreads) norm_few_kernel(const __grid_cons
   for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (tid % L == 0) own_sum[tid / L] = sum;
   __syncthreads();
+  if (p.cluster > 1) bsg::cluster_open_wait();
   if (tid < rows) {
     float s = own_sum[tid];
     for (int k = 1; k < slots; ++k) s += own_sum[k * rp + tid];
@@ -481,6 +484,7 @@ __global__ void __launch_bounds__(T, kBwdCtasPerSm<T, BF16>)
 #pragma unroll
   for (int v = 0; v < V; ++v) in[v] = run0 + v * tc * kVec < p.slice && c0 + v * tc * kVec < p.cols;
 
+  if (p.cluster > 1) bsg::cluster_open_arrive();
   bsg::grid_dependency_wait();
 
   float2 w[V][4], dw[V][4];
@@ -534,6 +538,7 @@ __global__ void __launch_bounds__(T, kBwdCtasPerSm<T, BF16>)
   int buf = 0;
   fetch(r, e, 0);
   float rs_next = r < p.rows ? __ldcg(p.rstd + r) : 0.f;
+  if (p.cluster > 1) bsg::cluster_open_wait();
   for (int64_t base = static_cast<int64_t>(part) * groups; base < p.rows; base += stride) {
     const bool exists = r < p.rows;
     if constexpr (!BF16) __syncwarp();   // the warp has read the buffer's last row

@@ -155,6 +155,7 @@ __global__ void __launch_bounds__((kThreads<G, BF16_IN>), (kMinCtasPerSm<G, BF16
   const int part = static_cast<int>(blockIdx.x % kP);
   const int64_t r0 = (blk / col_blocks) * G + part * (G / kP);
   const int64_t c0 = (blk % col_blocks) * G;
+  if constexpr (kP > 1) bsg::cluster_open_arrive();
   // the thread's runs stay in registers between the two passes
   constexpr int kHeld = kRuns / kT <= 8 ? kRuns / kT : 0;
   Run<BF16_IN> held[kHeld > 0 ? kHeld : 1];
@@ -226,7 +227,9 @@ __global__ void __launch_bounds__((kThreads<G, BF16_IN>), (kMinCtasPerSm<G, BF16
     // `part` of every CTA of the cluster, its own included. One cluster
     // barrier (every thread; release then acquire) makes all kP shares
     // visible in each CTA's own shared memory, and no CTA touches another's
-    // shared memory after it, so any CTA may then run on to its exit.
+    // shared memory after it, so any CTA may then run on to its exit. The
+    // barrier before the stores says that every CTA has begun to run.
+    bsg::cluster_open_wait();
     if (threadIdx.x == 0) {
       const uint32_t slot = static_cast<uint32_t>(__cvta_generic_to_shared(&part_max[part]));
 #pragma unroll

@@ -288,7 +288,19 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
-// Every thread of both CTAs of the cluster (all threads must execute it).
+// A CTA's shared memory may be written by another CTA of its cluster only once
+// it has begun to run, which being launched together does not say. So a kernel
+// that stores to a peer opens its cluster first: every thread arrives at the
+// kernel's start (nothing to publish: relaxed) and waits before the first such
+// store, with the first loads from global memory under way between the two.
+__device__ __forceinline__ void cluster_open_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_open_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Every thread of every CTA of the cluster (all threads must execute it).
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");

@@ -24,3 +24,30 @@ def test_no_read_only_loads_beside_a_running_writer():
         assert not re.search(r"__ldg\s*\(|ld\.global\.nc|ldu\.global|__restrict__", text), name
     # the other launches have no programmatic attribute, and begin after everything before them
     assert "ProgrammaticStreamSerialization" not in source("bsgemm_quant.cu") + source("bsgemm_noalloc.cu")
+
+
+def kernels(text):
+    """Name -> body of every kernel of a source."""
+    parts = re.split(r"__global__", text)[1:]
+    return {re.search(r"\b(\w+_kernel)\s*\(", part).group(1): part for part in parts}
+
+
+def test_clusters_are_open_before_a_store_to_a_peer():
+    """A peer's shared memory is written only past a cluster barrier: arrive, then wait, then the first remote store."""
+    found = []
+    for name in PROGRAMMATIC + ["bsgemm_quant.cu"]:
+        for kernel, body in kernels(source(name)).items():
+            store = re.search(r"\b(st_cluster_f32|st_shared_cluster_f32|mbar_arrive_cluster)\s*\(", body)
+            if store is None:
+                continue
+            found.append(kernel)
+            head = body[:store.start()]
+            opened = "cluster_sync_all(" in head
+            arrive, wait = head.find("cluster_open_arrive("), head.find("cluster_open_wait(")
+            assert opened or 0 <= arrive < wait, kernel
+            # the two halves are run by the same threads: under the same condition
+            if not opened:
+                def condition(at):
+                    return re.search(r"if (?:constexpr )?\(([^;{}]*)\)\s*(?:\{[^{}]*)?(?:bsg::)?$", head[:at]).group(1).strip()
+                assert condition(arrive) == condition(wait) or condition(wait) in ("kP > 1",), kernel
+    assert sorted(found) == ["block_quant_kernel", "bsgemm_pair_kernel", "norm_backward_kernel", "norm_few_kernel", "quant_kernel"]
