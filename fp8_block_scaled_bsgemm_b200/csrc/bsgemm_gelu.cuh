@@ -1,5 +1,6 @@
-// GELU in its erf form by one exponential, for the kernels whose arithmetic
-// would otherwise outlast their memory traffic or hold up the tensor core.
+// GELU in its erf form by one exponential, for the activation kernels, whose
+// arithmetic would otherwise outlast their memory traffic. (The GEMM's epilogue
+// evaluates 1 + erff, with a residual and without, in every plan.)
 #pragma once
 #include "ptx.cuh"
 

@@ -46,7 +46,6 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
-#include "bsgemm_gelu.cuh"
 #include "ptx.cuh"
 
 namespace bsg {
@@ -489,9 +488,8 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 // last store it waits for): the bias of the warp's columns goes through the buffer, from which every lane
 // reads it as broadcast 16-byte words. Loaded per lane and column, the same
 // values cost 128 dependent loads a tile (8192 x 14336 x 4096 with bias: 784
-// against 473 us without). FAST_GELU: the one-exponential form, within 2e-7 of
-// the value that erff gives.
-template <int NP, bool FAST_GELU>
+// against 473 us without).
+template <int NP>
 __device__ __forceinline__ void apply_epi_staged(const Params& p, uint32_t buf, int n0, float2 (&acc)[NP], uint32_t lane) {
   const int act = p.epi & 3;
   if (p.bias != nullptr) {
@@ -520,22 +518,9 @@ __device__ __forceinline__ void apply_epi_staged(const Params& p, uint32_t buf, 
 #pragma unroll
     for (int i = 0; i < NP; ++i) acc[i] = make_float2(fmaxf(acc[i].x, 0.f), fmaxf(acc[i].y, 0.f));
   } else if (act == kEpiGelu) {
-    if constexpr (FAST_GELU) {
 #pragma unroll
-      for (int i = 0; i < NP; i += 4) {
-        float2 z[4], n[4], tail[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) z[k] = acc[i + k];
-        bsgg::normal_tail(z, n, tail);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          acc[i + k] = ffma2(n[k], tail[k], make_float2(fmaxf(z[k].x, 0.f), fmaxf(z[k].y, 0.f)));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-        acc[i] = make_float2(epi_act_t<kEpiGelu>(acc[i].x), epi_act_t<kEpiGelu>(acc[i].y));
-    }
+    for (int i = 0; i < NP; ++i)
+      acc[i] = make_float2(epi_act_t<kEpiGelu>(acc[i].x), epi_act_t<kEpiGelu>(acc[i].y));
   }
 }
 
@@ -655,7 +640,7 @@ struct ResidualChunks {
                                                 uint32_t bar, int m0, int n0, ResidualState& s, float2 (&acc)[NP],
                                                 uint32_t lane) {
     if (p.residual == nullptr) {
-      apply_epi_staged<NP, false>(p, buf, n0, acc, lane);
+      apply_epi_staged<NP>(p, buf, n0, acc, lane);
       return true;
     }
     if (s.started == 0) start(tm, buf, bar, m0, n0, s.started++, lane);
@@ -663,7 +648,7 @@ struct ResidualChunks {
 #pragma unroll 1
       while (s.added < kChunks)
         if (!advance(p, bars, tm, buf, bar, m0, n0, s, acc, lane)) return false;
-      apply_epi_staged<NP, true>(p, buf, n0, acc, lane);
+      apply_epi_staged<NP>(p, buf, n0, acc, lane);
       return true;
     }
     // the residual comes after the activation: the first chunk moves to
@@ -672,7 +657,7 @@ struct ResidualChunks {
     s.phase ^= 1;
     uint4 v[8];
     take(buf, lane, v);
-    apply_epi_staged<NP, true>(p, buf, n0, acc, lane);
+    apply_epi_staged<NP>(p, buf, n0, acc, lane);
     if constexpr (kChunks > 1) start(tm, buf, bar, m0, n0, s.started++, lane);
     add(s.added++, v, acc);
 #pragma unroll 1
