@@ -30,12 +30,15 @@ using namespace bsgr;
 // cuts cross, so the work is done in two steps.
 //
 // Many rows: two kernels. The first streams the rows (h = x + residual, its
-// squares summed, rstd written) at the memory's rate: 30 us of the 45 us that
-// 8192 x 4096 BF16 with residual takes (0.79 of the copy rate over the bytes
+// squares summed, rstd written) at the memory's rate: 30 us of the 51 us that
+// 8192 x 4096 BF16 with residual takes (0.70 of the copy rate over the bytes
 // that have to move). The second reads h again, partly from L2 (x and residual
-// are read as first to leave it, h is kept as kKeepBytes says, and its rows go
-// from the last written to the first: 70.2 -> 61.2 us at g = 256), and is the
-// block kernel of bsgemm_blocks.cuh with y = h * rstd * weight for a value.
+// are read as first to leave it, and its rows go from the last written to the
+// first: 70.2 -> 61.2 us at g = 256), and is the block kernel of
+// bsgemm_blocks.cuh with y = h * rstd * weight for a value. h takes its usual
+// place in L2: stored as last to leave it, it saved 3.5 us in a loop of norms
+// alone, nothing where L2 held other data before, and the GEMM behind lost 2 us
+// (8192 x 14336 x 4096) to the lines that stayed.
 // Slabs of rows with two launches to each cost more than they save (32 MB
 // slabs: 58 us). One kernel that holds a row of blocks across a cluster of up to 16
 // CTAs, exchanging row sums through distributed shared memory between two
@@ -65,7 +68,6 @@ struct NormParams {
   int row_log;      // log2 of the rows a CTA's threads take at once (all of them)
   // many rows only
   int tc_log;       // log2 of the threads to a row
-  int keep;         // h is kept in L2 for the second kernel
 };
 
 __device__ __forceinline__ void load_weight(const void* weight, int is_bf16, int64_t c, float2 (&w)[4]) {
@@ -136,7 +138,6 @@ __global__ void __launch_bounds__(kRowThreads) norm_rows_kernel(const __grid_con
   bsg::grid_launch_dependents();
   bsg::grid_dependency_wait();
   const bool exists = r < p.rows;
-  const uint64_t place = l2_place(p.keep != 0);
   float2 s = both(0.f);
   if (exists) {
     const int64_t base = r * p.cols;
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_rows_kernel(const __grid_con
       for (int j = 0; j < U; ++j) {
         if constexpr (RES) {
           h[j] = add_runs<BF16>(h[j], res[j]);
-          store_run<BF16>(p.stream_out, base + c + j * stride, h[j], place);
+          store_run<BF16>(p.stream_out, base + c + j * stride, h[j]);
         }
         s = add_squares<BF16>(h[j], s);
       }
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_rows_kernel(const __grid_con
       Run<BF16> h = RES ? load_run_once<BF16>(p.x, base + c) : load_run<BF16>(p.x, base + c);
       if constexpr (RES) {
         h = add_runs<BF16>(h, load_run_once<BF16>(p.residual, base + c));
-        store_run<BF16>(p.stream_out, base + c, h, place);
+        store_run<BF16>(p.stream_out, base + c, h);
       }
       s = add_squares<BF16>(h, s);
     }
@@ -388,15 +389,6 @@ bsgemm_status few_of(int fmt, NormParams& p, cudaStream_t st, const bsg_host::De
                                 : few_of<G, BF16, BSGEMM_FP8_E4M3>(p, st, dev);
 }
 
-// A stream h of up to this size, half of L2, is stored as the last to leave it, so
-// that the second kernel finds it there. B200, BF16 with residual, g = 128, alone
-// and followed by a GEMM of N columns, without and with: 6144 x 4096 40.0 -> 36.3
-// us, N = 4096 144.7 -> 142.3; 8192 x 4096 50.4 -> 45.2, N = 4096 175.7 -> 172.6,
-// N = 8192 298.0 -> 298.7, N = 14336 490.6 -> 494.0 (h takes places from a GEMM
-// that is large enough). Past this size it gained less (8192 x 8192 100.5 -> 96.9)
-// and cost that much after it.
-constexpr int64_t kKeepBytes = 64ll << 20;
-
 template <bool BF16>
 bsgemm_status norm_of(int fmt, int gran, NormParams& p, cudaStream_t st, const bsg_host::DeviceInfo& dev) {
   if (gran == 64 && p.rows <= kFewRows<64>) return few_of<64, BF16>(fmt, p, st, dev);
@@ -408,7 +400,6 @@ bsgemm_status norm_of(int fmt, int gran, NormParams& p, cudaStream_t st, const b
   while ((1 << p.tc_log) < kRowThreads && (kVec << p.tc_log) < p.cols &&
          (p.rows << p.tc_log) < int64_t{dev.num_sms} * 1024)
     ++p.tc_log;
-  p.keep = p.rows * p.cols * (BF16 ? 2 : 4) <= kKeepBytes;
   const int64_t per_cta = kRowThreads >> p.tc_log;
   const int64_t ctas = (p.rows + per_cta - 1) / per_cta;
   bsgemm_status s = p.residual ? launch_rows<norm_rows_kernel<BF16, true>>(dev, ctas, kRowThreads, 0, 1, st, p)

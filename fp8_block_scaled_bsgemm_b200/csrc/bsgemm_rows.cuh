@@ -64,23 +64,6 @@ __device__ __forceinline__ void store_run(void* base, int64_t elem, const Run<BF
   for (int h = 0; h < (BF16 ? 1 : 2); ++h) p[h] = r.w[h];
 }
 
-// The same with a place in L2: among the last to leave, or the usual.
-__device__ __forceinline__ uint64_t l2_place(bool last_out) {
-  uint64_t last, normal;
-  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(last));
-  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
-  return last_out ? last : normal;
-}
-template <bool BF16>
-__device__ __forceinline__ void store_run(void* base, int64_t elem, const Run<BF16>& r, uint64_t place) {
-  uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + elem * (BF16 ? 2 : 4));
-#pragma unroll
-  for (int h = 0; h < (BF16 ? 1 : 2); ++h)
-    asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p + h), "r"(r.w[h].x), "r"(r.w[h].y),
-                 "r"(r.w[h].z), "r"(r.w[h].w), "l"(place)
-                 : "memory");
-}
-
 // The run's columns as four FP32 pairs (exact).
 template <bool BF16>
 __device__ __forceinline__ void widen(const Run<BF16>& r, float2 (&v)[4]) {

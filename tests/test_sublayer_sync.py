@@ -51,3 +51,9 @@ def test_clusters_are_open_before_a_store_to_a_peer():
                     return re.search(r"if (?:constexpr )?\(([^;{}]*)\)\s*(?:\{[^{}]*)?(?:bsg::)?$", head[:at]).group(1).strip()
                 assert condition(arrive) == condition(wait) or condition(wait) in ("kP > 1",), kernel
     assert sorted(found) == ["block_quant_kernel", "bsgemm_pair_kernel", "norm_backward_kernel", "norm_few_kernel", "quant_kernel"]
+
+
+def test_nothing_is_left_behind_in_l2():
+    """No kernel stores or reads data as the last to leave L2: the places would be lost to the kernels that follow."""
+    for name in os.listdir(CSRC):
+        assert not re.search(r"evict_last|createpolicy|persisting", source(name)), name
