@@ -6,7 +6,7 @@ path: if the library is missing (and cannot be built here) every call raises.
 The usual calls are marshalled in C++ (``_bsgemm_torch``, csrc/bsgemm_torch.cpp),
 which takes a third of the host time; what it does not take (outputs given, a
 stream given, another device, arguments to be refused) goes through the Python
-code here.
+code here, and so does everything where that module cannot be built or loaded.
 
     out = bsgemm_fp8_nt(a, b, scale_a, scale_b)          # a [M,K], b [N,K]
     out = gemm(a, b, scale_a, scale_b, layout="tn")      # a [K,M], b [K,N]
@@ -20,6 +20,7 @@ import contextlib
 import ctypes
 import os
 import threading
+import warnings
 
 import torch
 
@@ -88,10 +89,7 @@ def lib():
         if _lib is None:
             if not os.path.exists(LIB_PATH):
                 from . import build as _build
-                _build.build()
-            if not os.path.exists(os.path.join(_HERE, "_bsgemm_torch.so")):
-                from . import build as _build
-                _build.build_binding()
+                _build.build_library()
             L = ctypes.CDLL(LIB_PATH)
             p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
             gemm_args = [p, p, p, p, p, i64, i64, i64, i32, p]
@@ -144,15 +142,28 @@ def lib():
             L.bsgemm_activation_backward_workspace.restype = size
             L.bsgemm_version.argtypes = []
             L.bsgemm_version.restype = i32
-            from . import _bsgemm_torch
-            _bsgemm_torch.bind(*(ctypes.cast(getattr(L, name), p).value for name in _FAST_ENTRIES))
-            _fast = _bsgemm_torch
+            _fast = _load_marshalling(L)
             _lib = L
     return _lib
 
 
+def _load_marshalling(L):
+    """The C++ marshalling bound to the library ``L``, built first where it is missing or older than its source or
+    torch; None, with a warning, where that fails: the Python code then takes every call."""
+    try:
+        from . import build as _build
+        _build.build_binding()
+        from . import _bsgemm_torch
+        _bsgemm_torch.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _FAST_ENTRIES))
+        return _bsgemm_torch
+    except Exception as e:   # no compiler or headers, another torch's module: whatever it is, calls still work
+        warnings.warn(f"calls are marshalled in Python, which takes longer on the host: {str(e).strip()[:300]}",
+                      RuntimeWarning, stacklevel=4)
+        return None
+
+
 def _marshal():
-    """The C++ marshalling, with the library loaded; None where it is switched off."""
+    """The C++ marshalling, with the library loaded; None where there is none."""
     if _lib is None:
         lib()
     return _fast

@@ -89,7 +89,8 @@ def build_binding(force: bool = False) -> str:
     return BINDING
 
 
-def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
+def build_library(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
+    """``libbsgemm.so``, its units rebuilt where a source is newer than they are."""
     os.makedirs(BUILD, exist_ok=True)
     newest = _newest_source()
     units = [(os.path.join(CSRC, "bsgemm_api.cu"), os.path.join(BUILD, "bsgemm_api.o"), []),
@@ -121,6 +122,12 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stderr[-4000:])
         os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
+    """The library and the binding's marshalling module."""
+    build_library(force, jobs, verbose)
     build_binding(force)
     return LIB
 
