@@ -394,11 +394,18 @@ _HERE_AND_NOW = contextlib.nullcontext()
 def _on(device, stream):
     """A context in which ``device`` is current and, where a stream is given, that
     stream too, so that outputs and workspaces come from the memory of the
-    stream that the kernels run on (``_raw_stream`` then gives its handle)."""
+    stream that the kernels run on (``_raw_stream`` then gives its handle).
+    A stream is torch's, another object with its handle as ``cuda_stream``, or
+    the handle itself; one that is known to be another device's is refused."""
     if stream is None:
         return _HERE_AND_NOW if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    of = getattr(stream, "device", None)
+    if isinstance(of, torch.device) and of != device:
+        raise ValueError(f"stream is on {of}, the first operand on {device}")
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        # cudaStreamLegacy (1) is the stream 0 under a name that torch does not know
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
     return torch.cuda.stream(stream)   # makes the stream's device current as well
 
 

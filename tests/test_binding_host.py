@@ -56,3 +56,50 @@ def test_a_missing_library_is_built_without_the_module(monkeypatch):
     assert calls == []
     build.build()
     assert calls == [False]
+
+
+class Streams:
+    """Stand-ins for torch's streams on a machine without a GPU; records what is made current."""
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.cuda_stream, self.device = handle, device
+
+    def __init__(self, monkeypatch, torch):
+        self.current = []
+        monkeypatch.setattr(torch.cuda, "Stream", self.Stream)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", self.Stream)
+        monkeypatch.setattr(torch.cuda, "stream", lambda s: self.current.append(s) or s)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+
+class OnlyAHandle:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+def test_streams_are_taken_by_object_and_by_handle(monkeypatch):
+    import torch
+
+    import fp8_block_scaled_bsgemm_b200 as bsg
+    streams = Streams(monkeypatch, torch)
+    dev = torch.device("cuda", 0)
+    own = streams.Stream(0x10, dev)
+    bsg._on(dev, own)
+    assert streams.current.pop() is own
+    for given, handle in ((OnlyAHandle(0x20), 0x20), (0x30, 0x30), (OnlyAHandle(0), 0), (0, 0), (1, 0), (2, 2)):
+        bsg._on(dev, given)
+        made = streams.current.pop()
+        assert (made.cuda_stream, made.device) == (handle, dev)
+    assert bsg._on(dev, None) is bsg._HERE_AND_NOW
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    import torch
+
+    import fp8_block_scaled_bsgemm_b200 as bsg
+    streams = Streams(monkeypatch, torch)
+    other = streams.Stream(0x10, torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        bsg._on(torch.device("cuda", 0), other)
+    assert streams.current == []
