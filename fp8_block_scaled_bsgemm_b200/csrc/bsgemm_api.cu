@@ -153,10 +153,11 @@ bsgemm_status get_workspace(cudaStream_t stream, size_t ws_bytes, size_t n_count
     if (capturing) return BSGEMM_ERR_CUDA;
   }
   if (w.ws_bytes < ws_bytes) {
-    if (w.ws && w.in_graph) g_outgrown.push_back({dev, w.ws, 0});
+    if (w.ws && w.ws_in_graph) g_outgrown.push_back({dev, w.ws, 0});
     else if (w.ws && cudaFreeAsync(w.ws, stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
     w.ws = nullptr;
     w.ws_bytes = 0;
+    w.ws_in_graph = false;   // no graph knows the buffer that takes its place
     size_t want = ws_bytes + ws_bytes / 4;
     void* p = nullptr;
     if (cudaMallocAsync(&p, want, stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
@@ -164,10 +165,11 @@ bsgemm_status get_workspace(cudaStream_t stream, size_t ws_bytes, size_t n_count
     w.ws_bytes = want;
   }
   if (w.n_counters < n_counters) {
-    if (w.counters && w.in_graph) g_outgrown.push_back({dev, w.counters, w.n_counters});
+    if (w.counters && w.counters_in_graph) g_outgrown.push_back({dev, w.counters, w.n_counters});
     else if (w.counters && cudaFreeAsync(w.counters, stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
     w.counters = nullptr;
     w.n_counters = 0;
+    w.counters_in_graph = false;
     size_t want = n_counters < 1024 ? 1024 : n_counters * 2;
     void* p = nullptr;
     if (cudaMallocAsync(&p, want * sizeof(int), stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
@@ -175,7 +177,10 @@ bsgemm_status get_workspace(cudaStream_t stream, size_t ws_bytes, size_t n_count
     if (cudaMemsetAsync(w.counters, 0, want * sizeof(int), stream) != cudaSuccess) return BSGEMM_ERR_CUDA;
     w.n_counters = want;
   }
-  if (capturing) w.in_graph = true;
+  if (capturing) {
+    w.ws_in_graph |= ws_bytes > 0;
+    w.counters_in_graph |= n_counters > 0;
+  }
   out = w;
   return BSGEMM_OK;
 } catch (const std::bad_alloc&) {   // of the host's maps

@@ -43,7 +43,9 @@ struct Workspace {
   size_t ws_bytes = 0;
   int* counters = nullptr;
   size_t n_counters = 0;
-  bool in_graph = false;   // a captured call uses these buffers: growing keeps them
+  // a captured call uses this very buffer: growing keeps it
+  bool ws_in_graph = false;
+  bool counters_in_graph = false;
 };
 
 // 2D tensor map with 128-byte swizzle; `inner` is the contiguous extent.
