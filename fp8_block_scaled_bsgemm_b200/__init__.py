@@ -72,7 +72,7 @@ class Plan(ctypes.Structure):
 
 EXPORTS = ("bsgemm_fp8_nt", "bsgemm_fp8_tn", "bsgemm_fp8_nn", "bsgemm_fp8_tt", "bsgemm_fp8_gemm_ex",
            "bsgemm_fp8_gemm_fmt", "bsgemm_fp8_gemm_fused", "bsgemm_fp8_grouped_nt",
-           "bsgemm_make_plan", "bsgemm_status_string", "bsgemm_get_last_device_status",
+           "bsgemm_make_plan", "bsgemm_make_plan_residual", "bsgemm_status_string", "bsgemm_get_last_device_status",
            "bsgemm_last_device_status_detail", "bsgemm_diag_wait_timeout", "bsgemm_version",
            "bsgemm_fp8_nt_noalloc", "bsgemm_quantize_fp8", "bsgemm_release_workspaces",
            "bsgemm_fp8_gemm_residual", "bsgemm_rms_norm_quantize_fp8", "bsgemm_rms_norm_backward",
@@ -108,9 +108,9 @@ def lib():
             L.bsgemm_fp8_gemm_fused.restype = i32
             L.bsgemm_fp8_grouped_nt.argtypes = [i32, i32, p, p, p, p, p, p, i32, i64, i64, i64, i32, p]
             L.bsgemm_fp8_grouped_nt.restype = i32
-            L.bsgemm_make_plan.argtypes = [i32, i64, i64, i64, i32, i32, ctypes.POINTER(Tuning),
-                                           ctypes.POINTER(Plan)]
-            L.bsgemm_make_plan.restype = i32
+            for make in (L.bsgemm_make_plan, L.bsgemm_make_plan_residual):
+                make.argtypes = [i32, i64, i64, i64, i32, i32, ctypes.POINTER(Tuning), ctypes.POINTER(Plan)]
+                make.restype = i32
             L.bsgemm_status_string.argtypes = [i32]
             L.bsgemm_status_string.restype = ctypes.c_char_p
             L.bsgemm_get_last_device_status.argtypes = [p]
@@ -634,9 +634,11 @@ def scratch_bytes(plan: dict) -> int:
     return 0
 
 
-def make_plan(M, N, K, gran=128, layout="nt", num_sms=148, tuning=None) -> dict:
+def make_plan(M, N, K, gran=128, layout="nt", num_sms=148, tuning=None, residual=False) -> dict:
+    """What a call of these sizes launches; ``residual``: one with a residual."""
     pl = Plan()
-    st = lib().bsgemm_make_plan(LAYOUTS[layout], M, N, K, gran, num_sms, _tuning(tuning), ctypes.byref(pl))
+    make = lib().bsgemm_make_plan_residual if residual else lib().bsgemm_make_plan
+    st = make(LAYOUTS[layout], M, N, K, gran, num_sms, _tuning(tuning), ctypes.byref(pl))
     if st != 0:
         raise BsgemmError(st, "bsgemm_make_plan")
     return pl.as_dict()

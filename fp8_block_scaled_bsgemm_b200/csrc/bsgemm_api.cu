@@ -406,9 +406,6 @@ extern "C" bsgemm_status bsgemm_make_plan(int layout, int64_t M, int64_t N, int6
   return BSGEMM_OK;
 }
 
-// ------------------------------------------------------------------ entry points
-namespace {
-
 // The automatic plan of a call with a residual, where it differs from the plain
 // call's: at g = 128 the epilogue's whole-tile instances promote faster than
 // their CTA pairs and stream-K instances, so those need a larger saving to pay.
@@ -418,9 +415,12 @@ namespace {
 // (4096 x 4096 x 8192), where it saves 0.4 % 469 against 430 (8192 x 4096 x
 // 14336); pairs against single CTAs 271 against 250 (2048 x 4096 x 32768). At
 // g = 64 stream-K stays ahead (114 against 122, 2048 x 4096 x 8192).
-bsgemm_status residual_plan(int layout, int64_t M, int64_t N, int64_t K, int gran, int num_sms, bsgemm_plan* pl) {
-  bsgemm_status st = bsgemm_make_plan(layout, M, N, K, gran, num_sms, nullptr, pl);
-  if (st != BSGEMM_OK || gran != 128) return st;
+extern "C" bsgemm_status bsgemm_make_plan_residual(int layout, int64_t M, int64_t N, int64_t K, int gran,
+                                                   int num_sms, const bsgemm_tuning* tuning, bsgemm_plan* pl) {
+  bsgemm_status st = bsgemm_make_plan(layout, M, N, K, gran, num_sms, tuning, pl);
+  // a tuning without a choice is none
+  const bool chosen = tuning && (tuning->variant || tuning->bnq || tuning->splits || tuning->stream_k);
+  if (st != BSGEMM_OK || chosen || gran != 128) return st;
   bsgemm_tuning t{};
   if (pl->cta_pair) {
     t.variant = BSGEMM_VARIANT_DATA_PARALLEL;
@@ -440,6 +440,9 @@ bsgemm_status residual_plan(int layout, int64_t M, int64_t N, int64_t K, int gra
   }
   return st;
 }
+
+// ------------------------------------------------------------------ entry points
+namespace {
 
 bsgemm_status gemm_call(int layout, int a_format, int b_format, const void* a, const void* b,
                         const float* scale_a, const float* scale_b, const bsgemm_epilogue* epi,
@@ -473,8 +476,7 @@ bsgemm_status gemm_call(int layout, int a_format, int b_format, const void* a, c
   st = device_info(dev);
   if (st != BSGEMM_OK) return st;
   bsgemm_plan pl;
-  st = residual && !tuning ? residual_plan(layout, M, N, K, gran, dev.num_sms, &pl)
-                           : bsgemm_make_plan(layout, M, N, K, gran, dev.num_sms, tuning, &pl);
+  st = (residual ? bsgemm_make_plan_residual : bsgemm_make_plan)(layout, M, N, K, gran, dev.num_sms, tuning, &pl);
   if (st != BSGEMM_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);

@@ -399,9 +399,15 @@ bsgemm_status bsgemm_fp8_grouped_nt(int a_format, int b_format, const void *a, c
                                     int64_t N, int64_t K, int gran, bsgemm_stream_t stream);
 
 /* Host-only: the plan a call with these sizes would use on a device with
- * `num_sms` SMs. Touches no device. */
+ * `num_sms` SMs. Touches no device. bsgemm_make_plan_residual is that of
+ * bsgemm_fp8_gemm_residual, which plans some sizes otherwise (at g = 128 whole
+ * tiles where the plain call pairs CTAs or splits off a small remainder);
+ * with any field of `tuning` set the two are alike. */
 bsgemm_status bsgemm_make_plan(int layout, int64_t M, int64_t N, int64_t K, int gran, int num_sms,
                                const bsgemm_tuning *tuning, bsgemm_plan *plan);
+bsgemm_status bsgemm_make_plan_residual(int layout, int64_t M, int64_t N, int64_t K, int gran,
+                                        int num_sms, const bsgemm_tuning *tuning,
+                                        bsgemm_plan *plan);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *bsgemm_status_string(bsgemm_status status);
