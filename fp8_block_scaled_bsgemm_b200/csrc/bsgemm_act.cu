@@ -9,9 +9,10 @@
 //            the two gradient products), dbias[n] = sum over rows of dz.
 //            The residual's gradient is dout itself.
 // Both run in the block kernel of bsgemm_blocks.cuh. B200, 8192 x 14336 BF16,
-// g = 128: GELU 66.7 us (0.80 of the copy rate), its gradient with dbias 109 us
-// (0.82), both held by instruction issue (two thirds of the slots taken); ReLU
-// is at the memory's rate (8192 x 8192: 30.6 us).
+// g = 128: GELU 74.7 us (0.72 of the copy rate), its gradient with dbias 117 us
+// (0.76), both held by instruction issue; ReLU is at the memory's rate (8192 x
+// 8192: 31.6 us, 0.97). Of the first two 7 us each are the quotients' correction
+// (bsgemm_rows.cuh), which gives the codes of the correctly rounded quotients.
 #include "bsgemm_blocks.cuh"
 #include "bsgemm_gelu.cuh"
 

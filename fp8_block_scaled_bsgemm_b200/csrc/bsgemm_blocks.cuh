@@ -78,14 +78,13 @@ __device__ __forceinline__ void fetch16(uint32_t dst, const char* src, bool in) 
   else
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
-// One run for each of L neighbouring threads, at `dst` + 16 bytes a thread. A
-// BF16 run is 16 bytes and its thread copies it. An FP32 run is two halves; if
-// its thread copied both, each copy of a warp would touch half of every 32-byte
-// sector and fetch it twice. So the group's 2 L halves are copied in order,
-// thread i taking halves i and i + L (L * 16 bytes on), and lie apart by parity:
-// first halves in T * 16 bytes, then second halves, in places flipped by 4 so
-// that neither the copies nor the reads meet in a bank. `src` is the thread's
-// first 16 bytes, `in` and `in2` whether its pieces exist.
+// One run for each of L neighbouring threads, in shared memory as in global
+// memory: 16 or 32 bytes a thread from `dst` on. A BF16 run is 16 bytes and its
+// thread copies it. An FP32 run is two halves; if its thread copied both, each
+// copy of a warp would touch half of every 32-byte sector and fetch it twice. So
+// the group's 2 L halves are copied in address order, thread i taking halves i
+// and i + L (L * 16 bytes on). `src` is the thread's first 16 bytes, `in` and
+// `in2` whether its pieces exist.
 template <bool BF16, bool WHOLE, int T, int L>
 __device__ __forceinline__ void fetch_run(uint32_t dst, int tid, const char* src, bool in, bool in2) {
   if constexpr (BF16) {
@@ -97,7 +96,9 @@ __device__ __forceinline__ void fetch_run(uint32_t dst, int tid, const char* src
     fetch16<WHOLE>(dst + L * 16, src + (in2 || WHOLE ? L * 16 : 0), in2);
   }
 }
-// The thread's run, past fetch_wait (and a __syncwarp for FP32).
+// The thread's run, past fetch_wait (and a __syncwarp for FP32). Of an FP32 run
+// every other group of four threads reads the second half first, so that the
+// eight threads of a bank cycle, 32 bytes apart, meet in no bank.
 template <bool BF16, int T>
 __device__ __forceinline__ Run<BF16> fetched_run(const uint4* at, int tid) {
   Run<BF16> r;

@@ -30,8 +30,8 @@ using namespace bsgr;
 // cuts cross, so the work is done in two steps.
 //
 // Many rows: two kernels. The first streams the rows (h = x + residual, its
-// squares summed, rstd written) at the memory's rate: 30 us of the 51 us that
-// 8192 x 4096 BF16 with residual takes (0.70 of the copy rate over the bytes
+// squares summed, rstd written) at the memory's rate: 30 us of the 53 us that
+// 8192 x 4096 BF16 with residual takes (0.68 of the copy rate over the bytes
 // that have to move). The second reads h again, partly from L2 (x and residual
 // are read as first to leave it, and its rows go from the last written to the
 // first: 70.2 -> 61.2 us at g = 256), and is the block kernel of
@@ -124,7 +124,7 @@ __device__ __forceinline__ float rstd_of(const NormParams& p, float sum) {
 }
 
 // Rows, 2^tc_log threads to each (32 at least): a thread walks its columns,
-// four runs in flight.
+// four BF16 runs or two FP32 runs in flight.
 constexpr int kRowThreads = 256;
 
 template <bool BF16, bool RES>
@@ -424,7 +424,7 @@ bsgemm_status norm_of(int fmt, int gran, NormParams& p, cudaStream_t st, const b
 // keeps the sums of dy * n of its 16 columns over all its rows; at the end they
 // are added over the CTA's row groups and written as one row of partial sums,
 // and a second kernel adds those rows in order (no atomics: the order never
-// changes). B200, BF16 with the skip path's gradient: 8192 x 4096 49.0 us (0.83
+// changes). B200, BF16 with the skip path's gradient: 8192 x 4096 50.7 us (0.81
 // of the copy rate over the bytes that have to move), where a barrier a row and
 // the sums at the end show, 32768 x 4096 167 us (0.98). Without the next row's
 // runs under way during a row's sum the first took 58.1 us.
