@@ -1182,10 +1182,10 @@ __global__ void __launch_bounds__(kNumThreads, 1)
         const bool in = kb < w.kb1;
         // (not by read-only loads: this kernel may begin while the one that
         // writes the scales, the norm or the activation in front of it, still runs)
-        const float a = in ? __ldcg(sp_row + kb) : 0.f;
+        const float a = in ? __ldca(sp_row + kb) : 0.f;
 #pragma unroll
         for (int j = 0; j < kNumGroups; ++j)
-          dst[j] = in ? a * __ldcg(p.sQ + static_cast<size_t>(qb[j]) * p.Kb + kb) : 0.f;
+          dst[j] = in ? a * __ldca(p.sQ + static_cast<size_t>(qb[j]) * p.Kb + kb) : 0.f;
       };
       load_chunk(w.kb0, sc_cur);
       load_chunk(w.kb0 + 32, sc_nxt);

@@ -320,10 +320,10 @@ __global__ void __launch_bounds__(kNumThreads, 1)
         const int kb = base + static_cast<int>(lane);
         const bool in = kb < p.Kb;
         // (not by read-only loads, as in bsgemm_kernel)
-        const float a = in ? __ldcg(sp_row + kb) : 0.f;
+        const float a = in ? __ldca(sp_row + kb) : 0.f;
 #pragma unroll
         for (int j = 0; j < kNumGroups; ++j)
-          dst[j] = in ? a * __ldcg(p.sQ + static_cast<size_t>(qb[j]) * p.Kb + kb) : 0.f;
+          dst[j] = in ? a * __ldca(p.sQ + static_cast<size_t>(qb[j]) * p.Kb + kb) : 0.f;
       };
       load_chunk(0, sc_cur);
       load_chunk(32, sc_nxt);
